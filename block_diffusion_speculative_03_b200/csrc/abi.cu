@@ -12,7 +12,9 @@
 #include "attn.cuh"
 #include "common.cuh"
 #include "gemm.cuh"
+#include "../../include/dflash_paged.h"
 #include "kernels.cuh"
+#include "paged.cuh"
 
 using namespace df;
 
@@ -231,7 +233,30 @@ struct dflash_cache {
     void* slab;
     long long s_kv, s_kind, s_layer, s_req;
     CUtensorMap tm_slab;
+    // sliding window of the attention over this cache (dflash_cache_set_window); 0: none
+    int window = 0, sinks = 0;
+    uint8_t* window_scratch = nullptr;
 };
+
+bool df::cache_view(const dflash_cache* c, CacheView& v) {
+    if (!c) return false;
+    const dflash_config& g = c->h->cfg;
+    const long long es = g.dtype == DFLASH_BF16 ? 2 : 4;
+    v.slab.slab = (uint8_t*)c->slab;
+    v.slab.s_req = c->s_req * es;
+    v.slab.s_layer = c->s_layer * es;
+    v.slab.s_kind = c->s_kind * es;
+    v.slab.s_kv = c->s_kv * es;
+    v.slab.len = c->len;
+    v.slab.committed = c->committed;
+    v.slab.batch = c->batch;
+    v.slab.capacity = c->capacity;
+    v.n_layers = g.n_layers;
+    v.n_kv_heads = g.n_kv_heads;
+    v.head_dim = g.head_dim;
+    v.dtype = g.dtype;
+    return true;
+}
 
 namespace {
 
@@ -669,6 +694,26 @@ int dflash_cache_set_len(dflash_cache* c, const int32_t* lens, dflash_stream str
     return cuda_status(cudaGetLastError());
 }
 
+int dflash_cache_set_window(dflash_cache* c, int window, int sinks, void* scratch, size_t bytes,
+                            dflash_stream stream) {
+    if (!c || window < 0 || sinks < 0) return DFLASH_INVALID_ARG;
+    if (window == 0) {
+        c->window = c->sinks = 0;
+        c->window_scratch = nullptr;
+        return DFLASH_OK;
+    }
+    if (c->h->cfg.dtype != DFLASH_BF16) return DFLASH_UNSUPPORTED;
+    if (!scratch || ((uintptr_t)scratch & 255)) return DFLASH_INVALID_ARG;
+    if (bytes < paged_scratch_bytes()) return DFLASH_WORKSPACE;
+    if (scratch != c->window_scratch &&
+        cudaMemsetAsync(scratch, 0, kPagedCounterBytes, S(stream)) != cudaSuccess)
+        return DFLASH_CUDA;
+    c->window = window;
+    c->sinks = sinks;
+    c->window_scratch = (uint8_t*)scratch;
+    return DFLASH_OK;
+}
+
 int dflash_cache_status(dflash_handle* h, dflash_cache* c, dflash_stream stream) {
     if (!h || !c || c->h != h) return DFLASH_INVALID_ARG;
     if (cudaStreamSynchronize(S(stream)) != cudaSuccess) return DFLASH_CUDA;
@@ -856,6 +901,33 @@ static int layers_bf16(dflash_handle* h, dflash_cache* cc, int gamma, bool inges
     ap.status = h->status;
     ap.causal = ingest ? 1 : 0;
     const int attn_blocks = splits * c.n_kv_heads * B;
+    PagedAttnParams wp;   // the same rows through the windowed attention (dflash_cache_set_window)
+    std::memset(&wp, 0, sizeof(wp));
+    if (cc->window > 0) {
+        wp.tmap = cc->tm_slab;
+        wp.slab = cc->slab;
+        wp.q = h->q;
+        wp.q_stride = Nq;
+        wp.out = h->o;
+        wp.len = cc->len;
+        wp.req_ok = h->req_ok;
+        wp.n = wp.max_seqs = B;
+        wp.uniform = wp.max_rows = gamma;
+        wp.total_rows = M;
+        wp.G = ap.G;
+        wp.nq = c.n_q_heads;
+        wp.nkv = c.n_kv_heads;
+        wp.causal = ap.causal;
+        wp.window = cc->window;
+        wp.sinks = cc->sinks;
+        wp.rows_kv = ap.rows_kv;
+        wp.rows_kind = ap.rows_kind;
+        wp.rows_page = ap.rows_req;
+        wp.scale_log2 = ap.scale_log2;
+        wp.counters = (int*)cc->window_scratch;
+        wp.partial = (float*)(cc->window_scratch + kPagedCounterBytes);
+        wp.wait_status = h->status;
+    }
 
     capture_x(h, 0, M, st);
     for (int l = 0; l < c.n_layers; ++l) {
@@ -907,10 +979,15 @@ static int layers_bf16(dflash_handle* h, dflash_cache* cc, int gamma, bool inges
         }
         capture_stage(h, h->cap_q, h->q, l, M, Nq, st);
         if (ingest && l == c.n_layers - 1) break;   // the last layer's K/V are written
-        ap.layer = l;
-        // attention trace: 8 stamps per CTA (attn.cuh), past the wait at 1, merge done at 7
-        ap.trace = trace_slot(h, TK_ATTENTION, attn_blocks, 8, 1, 7);
-        {
+        if (cc->window > 0) {
+            wp.row_layer = l * ap.rows_layer;
+            Timed t(h, TK_ATTENTION, st);
+            if (launch_paged_attn_bf16(wp, d, h->num_sms, st)) return DFLASH_CUDA;
+            h->launches += 1;
+        } else {
+            ap.layer = l;
+            // attention trace: 8 stamps per CTA (attn.cuh), past the wait at 1, merge done at 7
+            ap.trace = trace_slot(h, TK_ATTENTION, attn_blocks, 8, 1, 7);
             Timed t(h, TK_ATTENTION, st);
             int e = launch_attention(ap, d, B, st, &h->launches);
             if (e) return DFLASH_CUDA;

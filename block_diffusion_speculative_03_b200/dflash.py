@@ -1,5 +1,5 @@
 """ctypes binding of libdflash (include/dflash.h, include/dflash_ablation.h,
-include/dflash_diag.h, include/dflash_policy.h).
+include/dflash_diag.h, include/dflash_policy.h, include/dflash_paged.h).
 
 Functions carry the C names and only marshal arguments: every step of the
 draft step runs in the library's CUDA kernels.  Pointers are passed as ints
@@ -52,6 +52,18 @@ class dflash_cache_info(C.Structure):
     _fields_ = [("batch", C.c_int), ("capacity", C.c_int), ("status", C.c_void_p), ("len", C.c_void_p),
                 ("committed", C.c_void_p), ("slab", C.c_void_p), ("stride_kv", C.c_int64),
                 ("stride_kind", C.c_int64), ("stride_layer", C.c_int64), ("stride_request", C.c_int64)]
+
+
+class dflash_pool_config(C.Structure):
+    _fields_ = [("n_layers", C.c_int), ("n_q_heads", C.c_int), ("n_kv_heads", C.c_int), ("head_dim", C.c_int),
+                ("dtype", C.c_int), ("n_pages", C.c_int), ("page_size", C.c_int), ("max_seqs", C.c_int),
+                ("max_len", C.c_int), ("reserved", C.c_int)]
+
+
+class dflash_pool_info(C.Structure):
+    _fields_ = [("max_pages", C.c_int), ("status", C.c_void_p), ("len", C.c_void_p), ("table", C.c_void_p),
+                ("refs", C.c_void_p), ("slab", C.c_void_p), ("stride_page", C.c_int64), ("stride_layer", C.c_int64),
+                ("stride_kind", C.c_int64), ("stride_kv", C.c_int64)]
 
 
 DFLASH_POLICY_MAX_CANDIDATES = 8
@@ -132,6 +144,24 @@ def lib():
         "dflash_gamma_policy_alpha": (i32, [C.POINTER(dflash_gamma_policy), C.POINTER(C.c_double)]),
         "dflash_gamma_policy_expected_tokens": (i32, [C.c_double, i32, C.POINTER(C.c_double)]),
         "dflash_gamma_policy_choose": (i32, [C.POINTER(dflash_gamma_policy), C.POINTER(i32)]),
+        "dflash_pool_bytes": (i32, [C.POINTER(dflash_pool_config), C.POINTER(sz)]),
+        "dflash_pool_init": (i32, [C.POINTER(dflash_pool_config), vp, sz, C.POINTER(vp), vp]),
+        "dflash_pool_release": (None, [vp]),
+        "dflash_pool_get_info": (i32, [vp, C.POINTER(dflash_pool_info)]),
+        "dflash_pool_status": (i32, [vp, vp]),
+        "dflash_pool_launch_count": (i64, [vp]),
+        "dflash_pool_set_tables": (i32, [vp, vp, vp, vp]),
+        "dflash_pages_reserve": (i32, [vp, vp, vp, i32, vp]),
+        "dflash_pages_fork": (i32, [vp, vp, vp, i32, i32, vp]),
+        "dflash_pages_free": (i32, [vp, vp, vp, i32, vp]),
+        "dflash_pages_compact": (i32, [vp, vp, vp]),
+        "dflash_pages_write": (i32, [vp, vp, i32, i32, vp, vp, i64, vp, vp, i32, i32, vp]),
+        "dflash_pages_advance": (i32, [vp, vp, vp, i32, vp]),
+        "dflash_pages_store": (i32, [vp, vp, vp, vp, i32, vp]),
+        "dflash_pages_load": (i32, [vp, vp, vp, vp, i32, vp]),
+        "dflash_paged_attention": (i32, [vp, vp, i32, i32, vp, i64, vp, vp, i32, i32, i32, i32, i32, vp, vp]),
+        "dflash_window_scratch_bytes": (i32, [C.POINTER(sz)]),
+        "dflash_cache_set_window": (i32, [vp, i32, i32, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -162,6 +192,15 @@ def exported_symbols() -> list:
             "dflash_diag_gemm_bf16_noalloc_status", "dflash_diag_step_trace", "dflash_diag_step_trace_records",
             "dflash_gamma_policy_init", "dflash_gamma_policy_observe", "dflash_gamma_policy_alpha",
             "dflash_gamma_policy_expected_tokens", "dflash_gamma_policy_choose"]
+
+
+def paged_symbols() -> list:
+    """The entry points of include/dflash_paged.h."""
+    return ["dflash_pool_bytes", "dflash_pool_init", "dflash_pool_release", "dflash_pool_get_info",
+            "dflash_pool_status", "dflash_pool_launch_count", "dflash_pool_set_tables", "dflash_pages_reserve",
+            "dflash_pages_fork", "dflash_pages_free", "dflash_pages_compact", "dflash_pages_write",
+            "dflash_pages_advance", "dflash_pages_store", "dflash_pages_load", "dflash_paged_attention",
+            "dflash_window_scratch_bytes", "dflash_cache_set_window"]
 
 
 def _chk(st: int, where: str, check: bool = True) -> int:
@@ -467,3 +506,99 @@ def dflash_gamma_policy_choose(p: dflash_gamma_policy) -> int:
     out = C.c_int()
     _chk(lib().dflash_gamma_policy_choose(C.byref(p), C.byref(out)), "dflash_gamma_policy_choose")
     return out.value
+
+
+# -- paged pool (include/dflash_paged.h) --------------------------------------------
+def dflash_pool_bytes(cfg: dflash_pool_config, check: bool = True):
+    n = C.c_size_t(0)
+    st = _chk(lib().dflash_pool_bytes(C.byref(cfg), C.byref(n)), "dflash_pool_bytes", check)
+    return n.value if st == 0 else st
+
+
+def dflash_pool_init(cfg: dflash_pool_config, mem: int, nbytes: int, stream: int = 0, check: bool = True):
+    p = C.c_void_p()
+    st = _chk(lib().dflash_pool_init(C.byref(cfg), mem, nbytes, C.byref(p), stream), "dflash_pool_init", check)
+    return p.value if st == 0 else st
+
+
+def dflash_pool_release(p: int) -> None:
+    lib().dflash_pool_release(p)
+
+
+def dflash_pool_get_info(p: int) -> dflash_pool_info:
+    info = dflash_pool_info()
+    _chk(lib().dflash_pool_get_info(p, C.byref(info)), "dflash_pool_get_info")
+    return info
+
+
+def dflash_pool_status(p: int, stream: int = 0) -> int:
+    return lib().dflash_pool_status(p, stream)
+
+
+def dflash_pool_launch_count(p: int) -> int:
+    return lib().dflash_pool_launch_count(p)
+
+
+def dflash_pool_set_tables(p: int, lens: int, table: int, stream: int = 0, check: bool = True) -> int:
+    return _chk(lib().dflash_pool_set_tables(p, lens, table, stream), "dflash_pool_set_tables", check)
+
+
+def dflash_pages_reserve(p: int, seqs: Optional[int], grow: int, n: int, stream: int = 0, check: bool = True) -> int:
+    return _chk(lib().dflash_pages_reserve(p, seqs, grow, n, stream), "dflash_pages_reserve", check)
+
+
+def dflash_pages_fork(p: int, src: int, dst: int, n: int, deep: bool = False, stream: int = 0,
+                      check: bool = True) -> int:
+    return _chk(lib().dflash_pages_fork(p, src, dst, n, 1 if deep else 0, stream), "dflash_pages_fork", check)
+
+
+def dflash_pages_free(p: int, seqs: Optional[int], keep: Optional[int], n: int, stream: int = 0,
+                      check: bool = True) -> int:
+    return _chk(lib().dflash_pages_free(p, seqs, keep, n, stream), "dflash_pages_free", check)
+
+
+def dflash_pages_compact(p: int, used: int, stream: int = 0, check: bool = True) -> int:
+    return _chk(lib().dflash_pages_compact(p, used, stream), "dflash_pages_compact", check)
+
+
+def dflash_pages_write(p: int, seqs: Optional[int], n: int, layer: int, k: int, v: int, stride: int,
+                       row_start: Optional[int], row_count: Optional[int], total_rows: int, max_rows: int,
+                       stream: int = 0, check: bool = True) -> int:
+    return _chk(lib().dflash_pages_write(p, seqs, n, layer, k, v, stride, row_start, row_count, total_rows, max_rows,
+                                         stream), "dflash_pages_write", check)
+
+
+def dflash_pages_advance(p: int, seqs: Optional[int], row_count: Optional[int], n: int, stream: int = 0,
+                         check: bool = True) -> int:
+    return _chk(lib().dflash_pages_advance(p, seqs, row_count, n, stream), "dflash_pages_advance", check)
+
+
+def dflash_pages_store(p: int, seqs: Optional[int], c: int, reqs: Optional[int], n: int, stream: int = 0,
+                       check: bool = True) -> int:
+    return _chk(lib().dflash_pages_store(p, seqs, c, reqs, n, stream), "dflash_pages_store", check)
+
+
+def dflash_pages_load(p: int, seqs: Optional[int], c: int, reqs: Optional[int], n: int, stream: int = 0,
+                      check: bool = True) -> int:
+    return _chk(lib().dflash_pages_load(p, seqs, c, reqs, n, stream), "dflash_pages_load", check)
+
+
+def dflash_paged_attention(p: int, seqs: Optional[int], n: int, layer: int, q: int, q_stride: int,
+                           row_start: Optional[int], row_count: Optional[int], total_rows: int, max_rows: int,
+                           causal: bool, window: int, sinks: int, out: int, stream: int = 0,
+                           check: bool = True) -> int:
+    return _chk(lib().dflash_paged_attention(p, seqs, n, layer, q, q_stride, row_start, row_count, total_rows,
+                                             max_rows, 1 if causal else 0, window, sinks, out, stream),
+                "dflash_paged_attention", check)
+
+
+def dflash_window_scratch_bytes() -> int:
+    n = C.c_size_t(0)
+    _chk(lib().dflash_window_scratch_bytes(C.byref(n)), "dflash_window_scratch_bytes")
+    return n.value
+
+
+def dflash_cache_set_window(c: int, window: int, sinks: int, scratch: Optional[int], nbytes: int, stream: int = 0,
+                            check: bool = True) -> int:
+    return _chk(lib().dflash_cache_set_window(c, window, sinks, scratch, nbytes, stream), "dflash_cache_set_window",
+                check)

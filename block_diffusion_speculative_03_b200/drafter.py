@@ -38,6 +38,7 @@ class Cache:
         self._buf, self.ptr = _aligned_empty(self.nbytes, drafter.device)
         self.handle = D.dflash_cache_init(drafter.handle, self.ptr, self.nbytes, batch, capacity, _stream())
         self.info = D.dflash_cache_get_info(self.handle)
+        self._window_buf, self._window_ptr, self._window_bytes = None, None, 0
 
     def _i32(self, addr: int, n: int) -> torch.Tensor:
         base = self._buf.data_ptr()
@@ -64,6 +65,14 @@ class Cache:
     def set_len(self, lens: torch.Tensor) -> None:
         lens = lens.to(device=self.drafter.device, dtype=torch.int32).contiguous()
         D.dflash_cache_set_len(self.handle, lens.data_ptr(), _stream())
+
+    def set_window(self, window: int, sinks: int = 0) -> None:
+        """From now on draft_block (and ingest_fused_input) on this cache see only the last
+        `window` positions and the first `sinks` of the context; 0 turns the window off."""
+        if window > 0 and self._window_buf is None:
+            self._window_bytes = D.dflash_window_scratch_bytes()
+            self._window_buf, self._window_ptr = _aligned_empty(self._window_bytes, self.drafter.device)
+        D.dflash_cache_set_window(self.handle, window, sinks, self._window_ptr, self._window_bytes, _stream())
 
     def status(self) -> int:
         return D.dflash_cache_status(self.drafter.handle, self.handle, _stream())
@@ -125,6 +134,14 @@ class Drafter:
 
     def new_cache(self, batch: int, capacity: int) -> Cache:
         return Cache(self, batch, capacity)
+
+    def new_pool(self, n_pages: int, page_size: int, max_seqs: int, max_len: int):
+        """A paged pool (paging.PagePool) of this drafter's layers, heads and type."""
+        from .paging import PagePool
+        c = self.cfg
+        return PagePool(c.n_layers, c.n_q_heads, c.n_kv_heads, c.head_dim,
+                        "bf16" if self.torch_dtype == torch.bfloat16 else "f32", n_pages=n_pages,
+                        page_size=page_size, max_seqs=max_seqs, max_len=max_len, device=self.device)
 
     def launch_count(self) -> int:
         return D.dflash_launch_count(self.handle)
