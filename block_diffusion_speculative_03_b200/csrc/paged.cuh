@@ -61,7 +61,8 @@ int launch_pages_exchange(const PoolView& v, const int* seqs, const SlabView& c,
 // ---------------------------------------------------------------------------
 
 struct PagedAttnParams {
-    CUtensorMap tmap;        // bf16: rows of head_dim, 128-byte swizzle (box: see the kernels)
+    CUtensorMap tmap;        // bf16: slab rows as [head_dim / 64][rows][64], 128-byte swizzle, box
+                             // {64, min(page_size, 64), head_dim / 64}
     const void* slab;        // fp32: the slab itself
     const void* q;
     long long q_stride;      // elements
@@ -151,9 +152,15 @@ DF_DEV bool key_visible(int k, int pos, int hi, int window, int sinks) {
     return k < hi && (window <= 0 || k < sinks || k > pos - window);
 }
 
+// Tensor map of a bf16 slab of `rows` rows of d elements for the kernels (abi.cu); false
+// when the driver's encoder rejects it.
+bool encode_kv_rows(CUtensorMap* m, const void* slab, uint64_t rows, int d, int box_rows);
+
 size_t paged_scratch_bytes();    // partials and counters of an attention launch
 constexpr size_t kPagedCounterBytes = 8192;
 
+// At most 16 query rows per kv head (paged_decode.cu).
+int launch_paged_decode(const PagedAttnParams& p, int d, int num_sms, cudaStream_t st);
 int launch_paged_attn_f32(PagedAttnParams& p, int d, int num_sms, cudaStream_t st);
 int launch_paged_attn_bf16(PagedAttnParams& p, int d, int num_sms, cudaStream_t st);
 

@@ -6,7 +6,6 @@
 #include <new>
 
 #include "../../include/dflash_paged.h"
-#include "gemm.cuh"
 #include "paged.cuh"
 
 using namespace df;
@@ -15,7 +14,7 @@ struct dflash_pool {
     dflash_pool_config cfg;
     int device, num_sms;
     PoolView v;
-    CUtensorMap tmap;          // bf16: slab rows, box {64, min(page_size, 64)}
+    CUtensorMap tmap;          // bf16: the slab's rows (encode_kv_rows)
     uint8_t* scratch;          // attention partials and counters
     long long launches;
 };
@@ -148,7 +147,7 @@ int dflash_pool_init(const dflash_pool_config* cfg, void* mem, size_t bytes, dfl
     v.counters = (int*)(b + L.counters);
     if (c.dtype == DFLASH_BF16) {
         const uint64_t rows = (uint64_t)c.n_pages * 2 * c.n_layers * c.n_kv_heads * c.page_size;
-        if (!encode_bf16_2d(&p->tmap, v.slab, c.head_dim, rows, c.head_dim, std::min(c.page_size, 64))) {
+        if (!encode_kv_rows(&p->tmap, v.slab, rows, c.head_dim, std::min(c.page_size, 64))) {
             delete p;
             return DFLASH_CUDA;
         }

@@ -1,0 +1,448 @@
+// Attention of few query rows (at most 16 per kv head: one new token of up to 16
+// query heads per kv head, or a short block) over pages, bf16: split over the keys and
+// joined.
+//
+// With t_k = q.k log2(e) / sqrt(d), out = sum_k P_k v_k / sum_k 2^(t_k - b), P_k =
+// bf16(2^(t_k - b)) for an integer b per row.  b follows the running maximum and may
+// lag it by 8: moving b scales everything by an exact power of two, so the split points
+// and the order of the keys change no rounding of P.
+//
+// Bound by HBM: every K and V byte is read once, and there are only 2 * rows flops for
+// each.  So all SMs stream equal shares whatever the lengths: the 64-key tiles of all
+// (entry, kv head) pairs form one line of units, CTA p of P takes the units
+// [p U / P, (p+1) U / P), and a share may start or end inside a pair.  A pair held by
+// one CTA is finished there; otherwise its CTAs write partials (b, l, o) and the last to
+// arrive adds them in the order of the keys (nobody waits).
+//
+//   warp 0     TMA: K and V boxes of min(page_size, 64) rows (both 64-column halves of a
+//              row group in one box) into a ring; pages are looked up 32 at a time.
+//              Boxes in which no row sees a key are not loaded.
+//   warps 1-4  16 keys of every tile each, with their own running state: S = Q K^T and
+//              O += P V on m16n8k16 tensor instructions, P staying in registers (the
+//              accumulator layout of S is the operand layout of P).  No barrier between
+//              the warps until the end of the pair.  (At 16 rows the tensor work is 1/8 of
+//              what the loads leave time for, so the register path wins over tensor memory:
+//              no hand-offs between issuing, softmax and correction.)
+#include <algorithm>
+
+#include "paged.cuh"
+
+namespace df {
+
+namespace {
+
+constexpr int kThreads = 160;
+constexpr int kConsumers = 4;
+constexpr int kTileKeys = 64;
+constexpr float kBaseLag = 8.0f;
+
+template <int D> struct DecodeCfg {
+    static constexpr int TILE = kTileKeys * D * 2;           // bytes of a K (or V) tile
+    static constexpr int STAGES = D == 128 ? 5 : 10;
+    static constexpr int RING = STAGES * 2 * TILE;
+    static constexpr int OLD = D + 4;                        // row stride of the join buffer (floats)
+    static constexpr int JOIN = kConsumers * 16 * OLD * 4;
+    static constexpr int ENTRIES = kPoolMaxSeqs * 20 + 16;   // int4 + prefix per entry
+    static constexpr int SMEM = 1024 + RING + JOIN + kConsumers * 16 * 8 + ENTRIES + 256;
+    static constexpr int SLOT = 16 * (D + 2);                // floats of a partial
+};
+
+DF_DEV void ldsm4(uint32_t a, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+DF_DEV void ldsm4t(uint32_t a, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+DF_DEV void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+DF_DEV void tma_load_3d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y, int z, uint64_t pol) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1, {%2, %3, %4}], [%5], %6;"
+        ::"r"(smem_u32(dst)), "l"((uint64_t)m), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(pol)
+        : "memory");
+}
+
+// One CTA's stretch of one (entry, kv head) pair.
+struct Segment {
+    int i, g, t0, t1, nt;     // entry, kv head, key tiles [t0, t1) of nt
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_constant__ PagedAttnParams p) {
+    using C = DecodeCfg<D>;
+    constexpr int S = C::STAGES, NT8 = D / 8;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = smem_align_up<uint8_t>(smem_raw, 1024);
+    float* join = (float*)(ring + C::RING);                          // [kConsumers][16][OLD]
+    float2* join_ml = (float2*)(ring + C::RING + C::JOIN);           // [kConsumers][16]
+    int4* ent = (int4*)(join_ml + kConsumers * 16);                  // [n]: sequence, first row, rows, length
+    int* pre = (int*)(ent + kPoolMaxSeqs);                           // [n + 1]: tiles before entry i
+    uint64_t* full = (uint64_t*)(pre + kPoolMaxSeqs + 4);
+    uint64_t* empty = full + S;
+    __shared__ int abort_s, sums[8], flag_s;
+    volatile int* abort_flag = &abort_s;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], kConsumers);
+        }
+        abort_s = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&p.tmap);
+    }
+    griddep_wait();
+    griddep_launch();
+
+    // Entries and the prefix sum of their tiles; rows of bad ones are zeroed by one CTA each.
+    int run = 0;
+    for (int base = 0; base < p.n; base += kThreads) {
+        const int i = base + tid;
+        int nt = 0;
+        if (i < p.n) {
+            const AttnEntry e = attn_entry(p, i);
+            if (e.bad && i % (int)gridDim.x == (int)blockIdx.x) {
+                if (p.status) set_error(p.status, e.bad);
+                uint4* o = (uint4*)((__nv_bfloat16*)p.out + (size_t)e.start * p.nq * D);
+                const size_t nz = (size_t)e.count * p.nq * D / 8;
+                for (size_t x = 0; x < nz; ++x) o[x] = make_uint4(0, 0, 0, 0);
+            }
+            if (!e.bad && e.count > 0)
+                nt = key_span(e.len, e.count, 0, e.count, p.causal, p.window, p.sinks, kTileKeys).nt;
+            ent[i] = make_int4(e.seq, e.start, e.count, e.len);
+        }
+        int inc = nt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += u;
+        }
+        if (lane == 31) sums[warp] = inc;
+        __syncthreads();
+        int before = run;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += sums[w];
+            run += sums[w];
+        }
+        if (i < p.n) pre[i] = before + inc - nt;
+        __syncthreads();
+    }
+    if (tid == 0) pre[p.n] = run;
+    __syncthreads();
+
+    const long long U = (long long)run * p.nkv;
+    // a share of at least two tiles: less is all latency
+    const int P = (int)min((long long)gridDim.x, max(1ll, U / 2));
+    if (U == 0 || (int)blockIdx.x >= P) return;
+    const long long u_begin = (long long)blockIdx.x * U / P, u_end = (long long)(blockIdx.x + 1) * U / P;
+
+    // entry that holds unit u: the last i with pre[i] * nkv <= u
+    int i0 = 0;
+    for (int lo = 0, hi = p.n; hi - lo > 1;) {
+        const int mid = (lo + hi) >> 1;
+        if ((long long)pre[mid] * p.nkv <= u_begin) lo = mid;
+        else hi = mid;
+        i0 = lo;
+    }
+    auto segment = [&](long long u, int& i) -> Segment {
+        while ((long long)pre[i + 1] * p.nkv <= u) ++i;      // u < U ends it
+        Segment s;
+        s.i = i;
+        s.nt = pre[i + 1] - pre[i];
+        const long long local = u - (long long)pre[i] * p.nkv;
+        s.g = (int)(local / s.nt);
+        s.t0 = (int)(local % s.nt);
+        s.t1 = (int)min((long long)s.nt, s.t0 + (u_end - u));
+        return s;
+    };
+    const int bl = p.table ? min(p.ps_log2, 6) : 6;          // log2 rows of a TMA box
+    const int box_rows = 1 << bl, boxes = kTileKeys >> bl;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer
+        const uint64_t pol = make_l2_policy_evict_first();
+        int it = 0, i = i0;
+        bool ok = true;
+        for (long long u = u_begin; u < u_end && ok;) {
+            const Segment s = segment(u, i);
+            const int4 e = ent[s.i];
+            const KeySpan span = key_span(e.w, e.z, 0, e.z, p.causal, p.window, p.sinks, kTileKeys);
+            const int hi = e.w + e.z, lo = p.window > 0 ? max(0, e.w - p.window + 1) : 0;
+            int pg0 = -1000000, pid = 0;                     // pages pg0 .. pg0 + 31, one per lane
+            for (int t = s.t0; t < s.t1; ++t, ++it) {
+                const int k0 = span.tile(t) * kTileKeys, st = it % S;
+                const int first = p.table ? k0 >> p.ps_log2 : 0;
+                if (p.table && (first < pg0 || first + boxes > pg0 + 32)) {
+                    pg0 = first;
+                    pid = pg0 + lane < p.max_pages ? p.table[(size_t)e.x * p.max_pages + pg0 + lane] : -1;
+                }
+                ok = mbar_wait(&empty[st], (uint32_t)(((it / S) & 1) ^ 1), abort_flag, p.wait_status);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                // lane b: box b of K, lane boxes + b: box b of V
+                const int b = lane & (boxes - 1), kind = lane / boxes, kb = k0 + b * box_rows;
+                const bool want = kind < 2 && kb < hi && (kb < p.sinks || kb + box_rows > lo);
+                const int page = p.table ? __shfl_sync(0xffffffffu, pid, ((kb >> p.ps_log2) - pg0) & 31) : e.x;
+                const int n_want = __popc(__ballot_sync(0xffffffffu, want && page >= 0));
+                if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(n_want * box_rows * D * 2));
+                __syncwarp();
+                if (want && page >= 0) {
+                    const long long row = (long long)page * p.rows_page + p.row_layer + (long long)s.g * p.rows_kv +
+                                          kind * p.rows_kind + (p.table ? kb & ((1 << p.ps_log2) - 1) : kb);
+                    tma_load_3d(ring + st * 2 * C::TILE + kind * C::TILE + b * box_rows * D * 2, &p.tmap, &full[st], 0,
+                                (int)row, 0, pol);
+                }
+            }
+            u += s.t1 - s.t0;
+        }
+        if (!ok) {
+            // an abandoned launch: its copies land before the CTA exits
+            volatile int never = 0;
+            for (int k = max(0, it - S); k < it; ++k) mbar_wait(&full[k % S], (uint32_t)((k / S) & 1), &never, nullptr);
+        }
+        return;
+    }
+
+    // ---------------------------------------------------------------- consumers
+    const int cw = warp - 1, c_tid = tid - 32;
+    const int qr = lane >> 2, qc = (lane & 3) * 2;            // accumulator row and first column of this lane
+    // ldmatrix row of this lane: K: matrices (keys 0-7, 8 columns), (keys 0-7, next 8), (keys 8-15, ..), ..;
+    // V transposed: (keys 0-7, columns), (keys 8-15, columns), (keys 0-7, next 8), ..
+    const int kk = cw * 16 + (lane & 7) + ((lane >> 4) << 3);
+    const int vk = cw * 16 + (lane & 7) + (((lane >> 3) & 1) << 3);
+    const int kc8 = (lane >> 3) & 1, vc8 = lane >> 4;         // which 16-byte column of a pair
+    auto row_addr = [&](int k) -> uint32_t {                  // byte offset of key k's first half in a tile
+        return (uint32_t)((k >> bl) * box_rows * D * 2 + (k & (box_rows - 1)) * 128);
+    };
+    const uint32_t k_off = row_addr(kk), v_off = row_addr(vk), half = (uint32_t)box_rows * 128;
+    const uint32_t ring_a = smem_u32(ring);
+
+    int it = 0, i = i0;
+    bool ok = true;
+    for (long long u = u_begin; u < u_end;) {
+        const Segment s = segment(u, i);
+        const int4 e = ent[s.i];
+        const KeySpan span = key_span(e.w, e.z, 0, e.z, p.causal, p.window, p.sinks, kTileKeys);
+        const int R = e.z * p.G, hi = e.w + e.z, lo = p.window > 0 ? max(0, e.w - p.window + 1) : 0;
+        // this lane's two rows: vector v = row * G + head
+        const int ra = qr / p.G, rb = (qr + 8) / p.G;
+        const int pos_a = e.w + ra, pos_b = e.w + rb;
+        const int hi_a = qr < R ? (p.causal ? pos_a + 1 : hi) : 0, hi_b = qr + 8 < R ? (p.causal ? pos_b + 1 : hi) : 0;
+        uint32_t qf[D / 16][4];
+        {
+            const __nv_bfloat16* q = (const __nv_bfloat16*)p.q;
+            const __nv_bfloat16* qa = q + (size_t)(e.y + ra) * p.q_stride + (size_t)(s.g * p.G + qr % p.G) * D + qc;
+            const __nv_bfloat16* qb = q + (size_t)(e.y + rb) * p.q_stride + (size_t)(s.g * p.G + (qr + 8) % p.G) * D + qc;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                qf[k][0] = qr < R ? *reinterpret_cast<const uint32_t*>(qa + k * 16) : 0u;
+                qf[k][2] = qr < R ? *reinterpret_cast<const uint32_t*>(qa + k * 16 + 8) : 0u;
+                qf[k][1] = qr + 8 < R ? *reinterpret_cast<const uint32_t*>(qb + k * 16) : 0u;
+                qf[k][3] = qr + 8 < R ? *reinterpret_cast<const uint32_t*>(qb + k * 16 + 8) : 0u;
+            }
+        }
+        float o[NT8][4];
+#pragma unroll
+        for (int j = 0; j < NT8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+        float base_a = -INFINITY, base_b = -INFINITY, l_a = 0.f, l_b = 0.f;
+
+        for (int t = s.t0; t < s.t1; ++t, ++it) {
+            const int st = it % S;
+            if (ok) ok = mbar_wait(&full[st], (uint32_t)((it / S) & 1), abort_flag, p.wait_status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) continue;
+            const int kw = span.tile(t) * kTileKeys + cw * 16;          // this warp's first key
+            const uint32_t sk = ring_a + st * 2 * C::TILE, sv = sk + C::TILE;
+            float sc[2][4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                uint32_t b[4];
+                ldsm4(sk + k_off + (k >> 2) * half + ((((k & 3) * 2 + kc8) ^ (kk & 7)) << 4), b);
+                mma16816(sc[0], qf[k], b[0], b[1]);
+                mma16816(sc[1], qf[k], b[2], b[3]);
+            }
+            // keys that some row does not see: the last ones, and with a window those before it
+            if (kw + 16 > (p.causal ? e.w + 1 : hi) ||
+                (p.window > 0 && kw + 16 > p.sinks && kw <= hi - 1 - p.window)) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int key = kw + j * 8 + qc + c;
+                        if (!key_visible(key, pos_a, hi_a, p.window, p.sinks)) sc[j][c] = -INFINITY;
+                        if (!key_visible(key, pos_b, hi_b, p.window, p.sinks)) sc[j][2 + c] = -INFINITY;
+                    }
+                // V rows that no row sees may hold anything (0 * NaN is NaN): zero them
+                const int key = kw + (lane >> 1);
+                const bool dead = key >= hi || (p.window > 0 && key >= p.sinks && key < lo);
+                if (dead) {
+                    uint8_t* vr = ring + st * 2 * C::TILE + C::TILE + row_addr(cw * 16 + (lane >> 1));
+#pragma unroll
+                    for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            *reinterpret_cast<uint4*>(vr + h * half + ((lane & 1) * 4 + c) * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async();      // before the slot's next TMA load
+                }
+                __syncwarp();
+            }
+            const float ma = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1])) * p.scale_log2;
+            const float mb = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3])) * p.scale_log2;
+            if (__any_sync(0xffffffffu, floorf(ma) > base_a + kBaseLag || floorf(mb) > base_b + kBaseLag)) {
+                float xa = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, 1));
+                float xb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
+                xa = floorf(fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 2)));
+                xb = floorf(fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 2)));
+                const float na = xa > base_a + kBaseLag ? xa : base_a, nb = xb > base_b + kBaseLag ? xb : base_b;
+                const float fa = na == base_a ? 1.f : exp2f(base_a - na), fb = nb == base_b ? 1.f : exp2f(base_b - nb);
+                base_a = na;
+                base_b = nb;
+                l_a *= fa;
+                l_b *= fb;
+#pragma unroll
+                for (int j = 0; j < NT8; ++j) {
+                    o[j][0] *= fa;
+                    o[j][1] *= fa;
+                    o[j][2] *= fb;
+                    o[j][3] *= fb;
+                }
+            }
+            const float za = base_a == -INFINITY ? 0.f : base_a, zb = base_b == -INFINITY ? 0.f : base_b;
+            uint32_t pf[4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float p0 = ex2_fast(fmaf(sc[j][0], p.scale_log2, -za)), p1 = ex2_fast(fmaf(sc[j][1], p.scale_log2, -za));
+                const float p2 = ex2_fast(fmaf(sc[j][2], p.scale_log2, -zb)), p3 = ex2_fast(fmaf(sc[j][3], p.scale_log2, -zb));
+                l_a += p0 + p1;
+                l_b += p2 + p3;
+                pf[j * 2] = pack_bf16(p0, p1);
+                pf[j * 2 + 1] = pack_bf16(p2, p3);
+            }
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+                uint32_t b[4];
+                ldsm4t(sv + v_off + (j >> 2) * half + ((((j & 3) * 2 + vc8) ^ (vk & 7)) << 4), b);
+                mma16816(o[2 * j], pf, b[0], b[1]);
+                mma16816(o[2 * j + 1], pf, b[2], b[3]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[st]);
+        }
+        // ---- join the warps
+        l_a += __shfl_xor_sync(0xffffffffu, l_a, 1);
+        l_b += __shfl_xor_sync(0xffffffffu, l_b, 1);
+        l_a += __shfl_xor_sync(0xffffffffu, l_a, 2);
+        l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
+        if ((lane & 3) == 0) {
+            join_ml[cw * 16 + qr] = make_float2(base_a, l_a);
+            join_ml[cw * 16 + qr + 8] = make_float2(base_b, l_b);
+        }
+#pragma unroll
+        for (int j = 0; j < NT8; ++j) {
+            if (qr < R) *reinterpret_cast<float2*>(join + (cw * 16 + qr) * C::OLD + j * 8 + qc) = make_float2(o[j][0], o[j][1]);
+            if (qr + 8 < R)
+                *reinterpret_cast<float2*>(join + (cw * 16 + qr + 8) * C::OLD + j * 8 + qc) = make_float2(o[j][2], o[j][3]);
+        }
+        named_bar_sync(1, kConsumers * 32);
+        const bool whole = s.t0 == 0 && s.t1 == s.nt;
+        const bool head = s.t0 == 0;                 // holds the pair's first tile
+        float* slot = p.partial + (size_t)(2 * blockIdx.x + (head ? 1 : 0)) * C::SLOT;
+        for (int x = c_tid; x < R * (D / 4); x += kConsumers * 32) {
+            const int r = x / (D / 4), c = (x % (D / 4)) * 4;
+            float B = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kConsumers; ++w) B = fmaxf(B, join_ml[w * 16 + r].x);
+            const float z = B == -INFINITY ? 0.f : B;
+            float L = 0.f;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kConsumers; ++w) {
+                const float2 ml = join_ml[w * 16 + r];
+                const float f = exp2f(ml.x - z);
+                const float4 v = *reinterpret_cast<const float4*>(join + (w * 16 + r) * C::OLD + c);
+                L += f * ml.y;
+                a.x += f * v.x;
+                a.y += f * v.y;
+                a.z += f * v.z;
+                a.w += f * v.w;
+            }
+            if (whole) {
+                const float inv = L == 0.f ? 0.f : 1.0f / L;
+                __nv_bfloat16* dst = (__nv_bfloat16*)p.out + ((size_t)(e.y + r / p.G) * p.nq + (size_t)s.g * p.G + r % p.G) * D + c;
+                *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+            } else {
+                *reinterpret_cast<float4*>(slot + 32 + r * D + c) = a;
+                if (c == 0) *reinterpret_cast<float2*>(slot + 2 * r) = make_float2(B, L);
+            }
+        }
+        if (!whole) {
+            // units of the pair [w0, w1) and the CTAs that hold them
+            const long long w0 = (long long)pre[s.i] * p.nkv + (long long)s.g * s.nt, w1 = w0 + s.nt;
+            const int c0 = (int)(((w0 + 1) * P - 1) / U), c1 = (int)((w1 * P - 1) / U);
+            __threadfence();
+            named_bar_sync(1, kConsumers * 32);
+            if (c_tid == 0) {
+                const int before = atomicAdd(&p.counters[c0], 1);
+                flag_s = before == c1 - c0;
+                if (before == c1 - c0) p.counters[c0] = 0;      // ready for the next launch
+            }
+            named_bar_sync(1, kConsumers * 32);
+            if (flag_s) {
+                __threadfence();
+                auto part = [&](int c) { return p.partial + (size_t)(2 * c + (c == c0 ? 1 : 0)) * C::SLOT; };
+                for (int x = c_tid; x < R * (D / 4); x += kConsumers * 32) {
+                    const int r = x / (D / 4), c = (x % (D / 4)) * 4;
+                    float B = -INFINITY;
+#pragma unroll 8
+                    for (int k = c0; k <= c1; ++k) B = fmaxf(B, __ldcg(part(k) + 2 * r));
+                    const float z = B == -INFINITY ? 0.f : B;
+                    float L = 0.f;
+                    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                    for (int k = c0; k <= c1; ++k) {
+                        const float* q = part(k);
+                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(q + 2 * r));
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(q + 32 + r * D + c));
+                        const float f = exp2f(ml.x - z);
+                        L += f * ml.y;
+                        a.x += f * v.x;
+                        a.y += f * v.y;
+                        a.z += f * v.z;
+                        a.w += f * v.w;
+                    }
+                    const float inv = L == 0.f ? 0.f : 1.0f / L;
+                    __nv_bfloat16* dst = (__nv_bfloat16*)p.out + ((size_t)(e.y + r / p.G) * p.nq + (size_t)s.g * p.G + r % p.G) * D + c;
+                    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+                }
+            }
+        }
+        named_bar_sync(1, kConsumers * 32);          // the join buffer and flag_s are free again
+        u += s.t1 - s.t0;
+    }
+}
+
+template <int D>
+int launch_d(const PagedAttnParams& p, int num_sms, cudaStream_t st) {
+    auto kern = k_paged_decode<D>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DecodeCfg<D>::SMEM) != cudaSuccess) return 1;
+    return (int)launch_k(kern, dim3(std::min(num_sms, kPagedCtas)), dim3(kThreads), DecodeCfg<D>::SMEM, st, p);
+}
+
+}  // namespace
+
+int launch_paged_decode(const PagedAttnParams& p, int d, int num_sms, cudaStream_t st) {
+    return d == 128 ? launch_d<128>(p, num_sms, st) : launch_d<64>(p, num_sms, st);
+}
+
+}  // namespace df
