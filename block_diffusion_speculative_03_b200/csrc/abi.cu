@@ -79,14 +79,14 @@ bool encode_bf16_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t r
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// K or V rows of d = 64 or 128 bf16 as [d / 64][rows][64]: one box {64, box_rows, d / 64}
-// brings box_rows whole rows, each 64-column half a block of 128-byte swizzled rows.
-bool encode_kv_rows(CUtensorMap* m, const void* slab, uint64_t rows, int d, int box_rows) {
+// K or V rows of d = 64 or 128 bf16 as [d / 64][rows][64]: a box {64, box_rows, halves}
+// brings box_rows rows, each 64-column half a block of 128-byte swizzled rows.
+bool encode_kv_rows(CUtensorMap* m, const void* slab, uint64_t rows, int d, int box_rows, int halves) {
     PFN_encodeTiled_t enc = get_encode();
     if (!enc || rows == 0 || ((uintptr_t)slab & 15)) return false;
     cuuint64_t dims[3] = {64, rows, (cuuint64_t)(d / 64)};
     cuuint64_t strides[2] = {(cuuint64_t)d * 2, 128};
-    cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)(d / 64)};
+    cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)halves};
     cuuint32_t es[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(slab), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -250,7 +250,7 @@ struct dflash_cache {
     // sliding window of the attention over this cache (dflash_cache_set_window); 0: none
     int window = 0, sinks = 0;
     uint8_t* window_scratch = nullptr;
-    CUtensorMap tm_window;
+    CUtensorMap tm_window, tm_window_half;
 };
 
 bool df::cache_view(const dflash_cache* c, CacheView& v) {
@@ -720,8 +720,10 @@ int dflash_cache_set_window(dflash_cache* c, int window, int sinks, void* scratc
     if (c->h->cfg.dtype != DFLASH_BF16) return DFLASH_UNSUPPORTED;
     if (!scratch || ((uintptr_t)scratch & 255)) return DFLASH_INVALID_ARG;
     if (bytes < paged_scratch_bytes()) return DFLASH_WORKSPACE;
-    if (!encode_kv_rows(&c->tm_window, c->slab, (uint64_t)c->batch * c->s_req / c->h->cfg.head_dim,
-                        c->h->cfg.head_dim, 64))
+    const int d = c->h->cfg.head_dim;
+    const uint64_t rows = (uint64_t)c->batch * c->s_req / d;
+    if (!encode_kv_rows(&c->tm_window, c->slab, rows, d, 64, d / 64) ||
+        !encode_kv_rows(&c->tm_window_half, c->slab, rows, d, 64, 1))
         return DFLASH_CUDA;
     if (scratch != c->window_scratch &&
         cudaMemsetAsync(scratch, 0, kPagedCounterBytes, S(stream)) != cudaSuccess)
@@ -923,6 +925,7 @@ static int layers_bf16(dflash_handle* h, dflash_cache* cc, int gamma, bool inges
     std::memset(&wp, 0, sizeof(wp));
     if (cc->window > 0) {
         wp.tmap = cc->tm_window;
+        wp.tmap_half = cc->tm_window_half;
         wp.slab = cc->slab;
         wp.q = h->q;
         wp.q_stride = Nq;

@@ -14,7 +14,7 @@ struct dflash_pool {
     dflash_pool_config cfg;
     int device, num_sms;
     PoolView v;
-    CUtensorMap tmap;          // bf16: the slab's rows (encode_kv_rows)
+    CUtensorMap tmap, tmap_half;   // bf16: the slab's rows (encode_kv_rows)
     uint8_t* scratch;          // attention partials and counters
     long long launches;
 };
@@ -147,7 +147,9 @@ int dflash_pool_init(const dflash_pool_config* cfg, void* mem, size_t bytes, dfl
     v.counters = (int*)(b + L.counters);
     if (c.dtype == DFLASH_BF16) {
         const uint64_t rows = (uint64_t)c.n_pages * 2 * c.n_layers * c.n_kv_heads * c.page_size;
-        if (!encode_kv_rows(&p->tmap, v.slab, rows, c.head_dim, std::min(c.page_size, 64))) {
+        const int box = std::min(c.page_size, 64), halves = c.head_dim / 64;
+        if (!encode_kv_rows(&p->tmap, v.slab, rows, c.head_dim, box, halves) ||
+            !encode_kv_rows(&p->tmap_half, v.slab, rows, c.head_dim, box, 1)) {
             delete p;
             return DFLASH_CUDA;
         }
@@ -291,6 +293,7 @@ int dflash_paged_attention(dflash_pool* p, const int32_t* seqs, int n, int layer
     PagedAttnParams a;
     std::memset(&a, 0, sizeof(a));
     a.tmap = p->tmap;
+    a.tmap_half = p->tmap_half;
     a.slab = p->v.slab;
     a.q = q;
     a.q_stride = q_stride;

@@ -266,8 +266,7 @@ int launch_paged_attn_f32(PagedAttnParams& p, int d, int num_sms, cudaStream_t s
     return d == 128 ? launch_simt<float, 128>(p, num_sms, st) : launch_simt<float, 64>(p, num_sms, st);
 }
 int launch_paged_attn_bf16(PagedAttnParams& p, int d, int num_sms, cudaStream_t st) {
-    if (p.max_rows * p.G <= 16) return launch_paged_decode(p, d, num_sms, st);
-    return d == 128 ? launch_simt<__nv_bfloat16, 128>(p, num_sms, st) : launch_simt<__nv_bfloat16, 64>(p, num_sms, st);
+    return p.max_rows * p.G <= 16 ? launch_paged_decode(p, d, num_sms, st) : launch_paged_block(p, d, num_sms, st);
 }
 
 }  // namespace df

@@ -8,11 +8,9 @@
 // and the order of the keys change no rounding of P.
 //
 // Bound by HBM: every K and V byte is read once, and there are only 2 * rows flops for
-// each.  So all SMs stream equal shares whatever the lengths: the 64-key tiles of all
-// (entry, kv head) pairs form one line of units, CTA p of P takes the units
-// [p U / P, (p+1) U / P), and a share may start or end inside a pair.  A pair held by
-// one CTA is finished there; otherwise its CTAs write partials (b, l, o) and the last to
-// arrive adds them in the order of the keys (nobody waits).
+// each.  So all SMs stream equal shares whatever the lengths (Line in paged.cuh).  An
+// item held by one CTA is finished there; otherwise its CTAs write partials (b, l, o) and
+// the last to arrive adds them in the order of the keys (nobody waits).
 //
 //   warp 0     TMA: K and V boxes of min(page_size, 64) rows (both 64-column halves of a
 //              row group in one box) into a ring; pages are looked up 32 at a time.
@@ -20,7 +18,7 @@
 //   warps 1-4  16 keys of every tile each, with their own running state: S = Q K^T and
 //              O += P V on m16n8k16 tensor instructions, P staying in registers (the
 //              accumulator layout of S is the operand layout of P).  No barrier between
-//              the warps until the end of the pair.  (At 16 rows the tensor work is 1/8 of
+//              the warps until the end of the item.  (At 16 rows the tensor work is 1/8 of
 //              what the loads leave time for, so the register path wins over tensor memory:
 //              no hand-offs between issuing, softmax and correction.)
 #include <algorithm>
@@ -33,7 +31,9 @@ namespace {
 
 constexpr int kThreads = 160;
 constexpr int kConsumers = 4;
-constexpr int kTileKeys = 64;
+constexpr int kTileKeys = kLineTile;
+constexpr int kOverhead = 2;   // units that starting and joining an item costs, in tiles
+constexpr int kMinShare = 4;   // smallest share of a CTA, in units
 constexpr float kBaseLag = 8.0f;
 
 template <int D> struct DecodeCfg {
@@ -42,8 +42,7 @@ template <int D> struct DecodeCfg {
     static constexpr int RING = STAGES * 2 * TILE;
     static constexpr int OLD = D + 4;                        // row stride of the join buffer (floats)
     static constexpr int JOIN = kConsumers * 16 * OLD * 4;
-    static constexpr int ENTRIES = kPoolMaxSeqs * 20 + 16;   // int4 + prefix per entry
-    static constexpr int SMEM = 1024 + RING + JOIN + kConsumers * 16 * 8 + ENTRIES + 256;
+    static constexpr int SMEM = 1024 + RING + JOIN + kConsumers * 16 * 8 + kLineBytes + 256;
     static constexpr int SLOT = 16 * (D + 2);                // floats of a partial
 };
 
@@ -69,11 +68,6 @@ DF_DEV void tma_load_3d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, i
         : "memory");
 }
 
-// One CTA's stretch of one (entry, kv head) pair.
-struct Segment {
-    int i, g, t0, t1, nt;     // entry, kv head, key tiles [t0, t1) of nt
-};
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_constant__ PagedAttnParams p) {
     using C = DecodeCfg<D>;
@@ -82,11 +76,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
     uint8_t* ring = smem_align_up<uint8_t>(smem_raw, 1024);
     float* join = (float*)(ring + C::RING);                          // [kConsumers][16][OLD]
     float2* join_ml = (float2*)(ring + C::RING + C::JOIN);           // [kConsumers][16]
-    int4* ent = (int4*)(join_ml + kConsumers * 16);                  // [n]: sequence, first row, rows, length
-    int* pre = (int*)(ent + kPoolMaxSeqs);                           // [n + 1]: tiles before entry i
-    uint64_t* full = (uint64_t*)(pre + kPoolMaxSeqs + 4);
+    uint8_t* line_mem = (uint8_t*)(join_ml + kConsumers * 16);
+    uint64_t* full = (uint64_t*)(line_mem + kLineBytes);
     uint64_t* empty = full + S;
-    __shared__ int abort_s, sums[8], flag_s;
+    __shared__ int abort_s, flag_s;
+    __shared__ long long sums[kThreads / 32];
     volatile int* abort_flag = &abort_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
@@ -101,97 +95,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
     griddep_wait();
     griddep_launch();
 
-    // Entries and the prefix sum of their tiles; rows of bad ones are zeroed by one CTA each.
-    int run = 0;
-    for (int base = 0; base < p.n; base += kThreads) {
-        const int i = base + tid;
-        int nt = 0;
-        if (i < p.n) {
-            const AttnEntry e = attn_entry(p, i);
-            if (e.bad && i % (int)gridDim.x == (int)blockIdx.x) {
-                if (p.status) set_error(p.status, e.bad);
-                uint4* o = (uint4*)((__nv_bfloat16*)p.out + (size_t)e.start * p.nq * D);
-                const size_t nz = (size_t)e.count * p.nq * D / 8;
-                for (size_t x = 0; x < nz; ++x) o[x] = make_uint4(0, 0, 0, 0);
-            }
-            if (!e.bad && e.count > 0)
-                nt = key_span(e.len, e.count, 0, e.count, p.causal, p.window, p.sinks, kTileKeys).nt;
-            ent[i] = make_int4(e.seq, e.start, e.count, e.len);
-        }
-        int inc = nt;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += u;
-        }
-        if (lane == 31) sums[warp] = inc;
-        __syncthreads();
-        int before = run;
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) before += sums[w];
-            run += sums[w];
-        }
-        if (i < p.n) pre[i] = before + inc - nt;
-        __syncthreads();
-    }
-    if (tid == 0) pre[p.n] = run;
-    __syncthreads();
-
-    const long long U = (long long)run * p.nkv;
-    // a share of at least two tiles: less is all latency
-    const int P = (int)min((long long)gridDim.x, max(1ll, U / 2));
+    Line line;
+    const long long U = line_plan<kThreads, D>(p, line, line_mem, sums, kOverhead);
+    const int P = (int)min((long long)gridDim.x, max(1ll, U / kMinShare));
     if (U == 0 || (int)blockIdx.x >= P) return;
-    const long long u_begin = (long long)blockIdx.x * U / P, u_end = (long long)(blockIdx.x + 1) * U / P;
-
-    // entry that holds unit u: the last i with pre[i] * nkv <= u
-    int i0 = 0;
-    for (int lo = 0, hi = p.n; hi - lo > 1;) {
-        const int mid = (lo + hi) >> 1;
-        if ((long long)pre[mid] * p.nkv <= u_begin) lo = mid;
-        else hi = mid;
-        i0 = lo;
-    }
-    auto segment = [&](long long u, int& i) -> Segment {
-        while ((long long)pre[i + 1] * p.nkv <= u) ++i;      // u < U ends it
-        Segment s;
-        s.i = i;
-        s.nt = pre[i + 1] - pre[i];
-        const long long local = u - (long long)pre[i] * p.nkv;
-        s.g = (int)(local / s.nt);
-        s.t0 = (int)(local % s.nt);
-        s.t1 = (int)min((long long)s.nt, s.t0 + (u_end - u));
-        return s;
-    };
+    Walker walk;
+    walk.start(line, blockIdx.x * U / P, (blockIdx.x + 1) * U / P);
+    Stretch s;
     const int bl = p.table ? min(p.ps_log2, 6) : 6;          // log2 rows of a TMA box
     const int box_rows = 1 << bl, boxes = kTileKeys >> bl;
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
         const uint64_t pol = make_l2_policy_evict_first();
-        int it = 0, i = i0;
+        int it = 0;
         bool ok = true;
-        for (long long u = u_begin; u < u_end && ok;) {
-            const Segment s = segment(u, i);
-            const int4 e = ent[s.i];
-            const KeySpan span = key_span(e.w, e.z, 0, e.z, p.causal, p.window, p.sinks, kTileKeys);
+        while (ok && walk.next(line, s)) {
+            const int4 e = line.ent[s.i];
             const int hi = e.w + e.z, lo = p.window > 0 ? max(0, e.w - p.window + 1) : 0;
-            int pg0 = -1000000, pid = 0;                     // pages pg0 .. pg0 + 31, one per lane
+            PageLookup look;
+            look.reset();
             for (int t = s.t0; t < s.t1; ++t, ++it) {
-                const int k0 = span.tile(t) * kTileKeys, st = it % S;
-                const int first = p.table ? k0 >> p.ps_log2 : 0;
-                if (p.table && (first < pg0 || first + boxes > pg0 + 32)) {
-                    pg0 = first;
-                    pid = pg0 + lane < p.max_pages ? p.table[(size_t)e.x * p.max_pages + pg0 + lane] : -1;
-                }
+                const int k0 = s.span.tile(t) * kTileKeys, st = it % S;
+                // lane b: box b of K, lane boxes + b: box b of V
+                const int b = lane & (boxes - 1), kind = lane / boxes, kb = k0 + b * box_rows;
+                const bool want = kind < 2 && kb < hi && (kb < p.sinks || kb + box_rows > lo);
+                const int page = look.at(p, e.x, k0, kb, boxes, lane);
                 ok = mbar_wait(&empty[st], (uint32_t)(((it / S) & 1) ^ 1), abort_flag, p.wait_status);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
                 }
-                // lane b: box b of K, lane boxes + b: box b of V
-                const int b = lane & (boxes - 1), kind = lane / boxes, kb = k0 + b * box_rows;
-                const bool want = kind < 2 && kb < hi && (kb < p.sinks || kb + box_rows > lo);
-                const int page = p.table ? __shfl_sync(0xffffffffu, pid, ((kb >> p.ps_log2) - pg0) & 31) : e.x;
                 const int n_want = __popc(__ballot_sync(0xffffffffu, want && page >= 0));
                 if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(n_want * box_rows * D * 2));
                 __syncwarp();
@@ -202,7 +136,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
                                 (int)row, 0, pol);
                 }
             }
-            u += s.t1 - s.t0;
         }
         if (!ok) {
             // an abandoned launch: its copies land before the CTA exits
@@ -226,12 +159,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
     const uint32_t k_off = row_addr(kk), v_off = row_addr(vk), half = (uint32_t)box_rows * 128;
     const uint32_t ring_a = smem_u32(ring);
 
-    int it = 0, i = i0;
+    int it = 0;
     bool ok = true;
-    for (long long u = u_begin; u < u_end;) {
-        const Segment s = segment(u, i);
-        const int4 e = ent[s.i];
-        const KeySpan span = key_span(e.w, e.z, 0, e.z, p.causal, p.window, p.sinks, kTileKeys);
+    while (walk.next(line, s)) {
+        const int4 e = line.ent[s.i];
         const int R = e.z * p.G, hi = e.w + e.z, lo = p.window > 0 ? max(0, e.w - p.window + 1) : 0;
         // this lane's two rows: vector v = row * G + head
         const int ra = qr / p.G, rb = (qr + 8) / p.G;
@@ -260,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
             if (ok) ok = mbar_wait(&full[st], (uint32_t)((it / S) & 1), abort_flag, p.wait_status);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) continue;
-            const int kw = span.tile(t) * kTileKeys + cw * 16;          // this warp's first key
+            const int kw = s.span.tile(t) * kTileKeys + cw * 16;          // this warp's first key
             const uint32_t sk = ring_a + st * 2 * C::TILE, sv = sk + C::TILE;
             float sc[2][4];
 #pragma unroll
@@ -355,8 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
                 *reinterpret_cast<float2*>(join + (cw * 16 + qr + 8) * C::OLD + j * 8 + qc) = make_float2(o[j][2], o[j][3]);
         }
         named_bar_sync(1, kConsumers * 32);
-        const bool whole = s.t0 == 0 && s.t1 == s.nt;
-        const bool head = s.t0 == 0;                 // holds the pair's first tile
+        const bool whole = s.whole(), head = s.t0 == 0;   // head: holds the item's first tile
         float* slot = p.partial + (size_t)(2 * blockIdx.x + (head ? 1 : 0)) * C::SLOT;
         for (int x = c_tid; x < R * (D / 4); x += kConsumers * 32) {
             const int r = x / (D / 4), c = (x % (D / 4)) * 4;
@@ -387,9 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
             }
         }
         if (!whole) {
-            // units of the pair [w0, w1) and the CTAs that hold them
-            const long long w0 = (long long)pre[s.i] * p.nkv + (long long)s.g * s.nt, w1 = w0 + s.nt;
-            const int c0 = (int)(((w0 + 1) * P - 1) / U), c1 = (int)((w1 * P - 1) / U);
+            // the CTAs that hold the item's first and last tile
+            const int c0 = line_owner(s.v0 + kOverhead, U, P), c1 = line_owner(s.v0 + kOverhead + s.span.nt - 1, U, P);
             __threadfence();
             named_bar_sync(1, kConsumers * 32);
             if (c_tid == 0) {
@@ -428,7 +357,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
             }
         }
         named_bar_sync(1, kConsumers * 32);          // the join buffer and flag_s are free again
-        u += s.t1 - s.t0;
     }
 }
 
@@ -441,7 +369,9 @@ int launch_d(const PagedAttnParams& p, int num_sms, cudaStream_t st) {
 
 }  // namespace
 
-int launch_paged_decode(const PagedAttnParams& p, int d, int num_sms, cudaStream_t st) {
+int launch_paged_decode(PagedAttnParams& p, int d, int num_sms, cudaStream_t st) {
+    p.rt = p.max_rows;
+    p.row_tiles = 1;
     return d == 128 ? launch_d<128>(p, num_sms, st) : launch_d<64>(p, num_sms, st);
 }
 
