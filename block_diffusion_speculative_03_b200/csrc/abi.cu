@@ -1004,7 +1004,7 @@ static int layers_bf16(dflash_handle* h, dflash_cache* cc, int gamma, bool inges
             wp.row_layer = l * ap.rows_layer;
             Timed t(h, TK_ATTENTION, st);
             if (launch_paged_attn_bf16(wp, d, h->num_sms, st)) return DFLASH_CUDA;
-            h->launches += 1;
+            h->launches += wp.launches;
         } else {
             ap.layer = l;
             // attention trace: 8 stamps per CTA (attn.cuh), past the wait at 1, merge done at 7

@@ -88,6 +88,7 @@ struct PagedAttnParams {
     int splits;              // fp32 kernel: key splits per item
     int* status;             // null: the slab path (requests are checked by the draft step)
     int* wait_status;        // DFLASH_TIMEOUT of a bounded wait
+    int launches;            // set by the launchers: kernels of this call
 };
 
 // Key tiles of TK keys that the rows [r0, r1) (positions len + r) of an entry with
@@ -361,6 +362,7 @@ bool encode_kv_rows(CUtensorMap* m, const void* slab, uint64_t rows, int d, int 
 
 size_t paged_scratch_bytes();    // partials and counters of an attention launch
 constexpr size_t kPagedCounterBytes = 8192;
+constexpr size_t kJoinRecords = 2048;   // in them: 32 bytes per CTA, what paged_block.cu has to join
 
 // At most 16 query rows per kv head (paged_decode.cu).
 int launch_paged_decode(PagedAttnParams& p, int d, int num_sms, cudaStream_t st);

@@ -327,7 +327,7 @@ int dflash_paged_attention(dflash_pool* p, const int32_t* seqs, int n, int layer
     a.wait_status = p->v.status;
     const int r = c.dtype == DFLASH_BF16 ? launch_paged_attn_bf16(a, c.head_dim, p->num_sms, S(stream))
                                          : launch_paged_attn_f32(a, c.head_dim, p->num_sms, S(stream));
-    return done(p, r, 1);
+    return done(p, r, a.launches);
 }
 
 int dflash_window_scratch_bytes(size_t* bytes) {

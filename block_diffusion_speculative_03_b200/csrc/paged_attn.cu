@@ -263,6 +263,7 @@ size_t paged_scratch_bytes() {
 }
 
 int launch_paged_attn_f32(PagedAttnParams& p, int d, int num_sms, cudaStream_t st) {
+    p.launches = 1;
     return d == 128 ? launch_simt<float, 128>(p, num_sms, st) : launch_simt<float, 64>(p, num_sms, st);
 }
 int launch_paged_attn_bf16(PagedAttnParams& p, int d, int num_sms, cudaStream_t st) {

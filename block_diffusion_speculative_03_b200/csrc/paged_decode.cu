@@ -372,6 +372,7 @@ int launch_d(const PagedAttnParams& p, int num_sms, cudaStream_t st) {
 int launch_paged_decode(PagedAttnParams& p, int d, int num_sms, cudaStream_t st) {
     p.rt = p.max_rows;
     p.row_tiles = 1;
+    p.launches = 1;
     return d == 128 ? launch_d<128>(p, num_sms, st) : launch_d<64>(p, num_sms, st);
 }
 
