@@ -325,6 +325,16 @@ struct Walker {
         return false;
     }
 };
+// True for one lane of a converged warp, the same one every time.
+DF_DEV bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
 // Whether an mbarrier phase has completed, without waiting.
 DF_DEV bool mbar_test(uint64_t* bar, uint32_t parity) {
     uint32_t ok;

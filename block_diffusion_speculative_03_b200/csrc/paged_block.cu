@@ -12,10 +12,10 @@
 //              joined once per stretch: two chains hide each other's latencies, and nothing is
 //              exchanged between warps inside a stretch).  Per tile: read the lane's slice of S,
 //              mask it where the tile has keys that some row does not see, write P =
-//              bf16(2^(t - b)) over S, rescale O by an exact power of two when b moves.
+//              bf16(2^(t - b)), rescale O by an exact power of two when b moves.
 //   warp 0     TMA: K and V tiles of 64 keys, one box per page and 64-column half.
-//   warp 1     tcgen05.mma: O += P V of a tile, then S = Q K^T of the group's next one (across
-//              the end of a stretch too: the next stretch's Q is already in the other buffer).
+//   warp 1     tcgen05.mma: once P of a tile is there, first S = Q K^T of the group's next tile
+//              (what its softmax waits for), then O += P V.
 //
 // An item that several CTAs hold is joined by a second launch (k_paged_join): adding up to 18
 // partials of 32 KB took one CTA 15 us, all SMs together 2 us.
@@ -42,8 +42,8 @@ template <int D> struct BlockCfg {
     static constexpr int JOIN = 128 * OLD * 4;
     static constexpr int SMEM = 1024 + RING + JOIN + 2 * 128 * 8 + kLineBytes + 512;
     static constexpr int SLOT = 128 * (D + 2);               // floats of a partial
-    // tensor memory columns: S[2] (64 each, P over its first 32), Q[2] (D / 2 bf16 pairs), O[2] (D)
-    static constexpr uint32_t T_S = 0, T_Q = 128, T_O = 256, COLS = 512;
+    // tensor memory columns: S[2] (64 each), P[2] (32 bf16 pairs each), Q (D / 2), O[2] (D each)
+    static constexpr uint32_t T_S = 0, T_P = 128, T_Q = 192, T_O = 256, COLS = 512;
 };
 
 template <int D, int CS>
@@ -61,8 +61,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
     uint64_t* s_full = kv_empty + S;                                 // [2]
     uint64_t* p_full = s_full + 2;                                   // [2]
     uint64_t* o_done = p_full + 2;                                   // [2]
-    uint64_t* q_full = o_done + 2;                                   // [2]
-    uint64_t* drain = q_full + 2;
+    uint64_t* q_full = o_done + 2;
+    uint64_t* drain = q_full + 1;
     uint32_t* tmem_slot = (uint32_t*)(drain + 1);
     __shared__ int abort_s;
     __shared__ long long sums[kThreads / 32];
@@ -78,8 +78,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 128);
             mbar_init(&o_done[i], 1);
-            mbar_init(&q_full[i], 128);
         }
+        mbar_init(q_full, 128);
         mbar_init(drain, 1);
         abort_s = 0;
         fence_mbar_init();
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
         tc_fence_after();
         tmem = *tmem_slot;
     }
-    const uint32_t tS = tmem + C::T_S, tQ = tmem + C::T_Q, tO = tmem + C::T_O;
+    const uint32_t tS = tmem + C::T_S, tP = tmem + C::T_P, tQ = tmem + C::T_Q, tO = tmem + C::T_O;
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
@@ -156,79 +156,88 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 64);
-            constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, true);
-            // S runs up to two tiles ahead of the products, on its own walk over the stretches, but
-            // at most one stretch ahead: the softmax brings the Q of stretch n + 1 when it begins
-            // stretch n, for which the products of stretch n - 1 must have been issued.  S of tile
-            // j + 2 overwrites P of tile j: it is issued once that tile's product is done.
-            Walker sw = walk;
-            Stretch ss;
-            int sj = 0, s_seg = -1, s_left = 0, seg = -1, it = 0;
-            bool more = true, ok = true;
-            auto s_step = [&]() {      // the next tile's S, if its stretch, Q and K are there
-                if (s_left == 0) {
-                    if (!more || s_seg > seg) return;
-                    more = sw.next(line, ss);
-                    if (!more) return;
-                    ++s_seg;
-                    s_left = ss.t1 - ss.t0;
-                }
-                const int st = sj % S;
-                if ((sj >= 2 && !mbar_test(&o_done[sj & 1], (uint32_t)(((sj - 2) >> 1) & 1))) ||
-                    !mbar_test(&q_full[s_seg & 1], (uint32_t)((s_seg >> 1) & 1)) ||
-                    !mbar_test(&kv_full[st], (uint32_t)((sj / S) & 1)))
-                    return;
-                tc_fence_after();
-                const uint32_t ka = smem_u32(ring + st * 2 * C::KV);
+        // The whole warp walks and waits, one elected lane issues: in code that the warp runs
+        // together the operands stay in uniform registers (128 x 64 x 16 measured 33 cycles an
+        // instruction against 47-70 in a branch of one lane).
+        constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 64);
+        constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, true);
+        const bool leader = elect_one();
+        // S runs ahead on its own walk over the stretches.  S of tile j + 2 goes where S of tile j
+        // was, once the softmax has read that (P of tile j is there); the first S of a stretch
+        // waits for its Q, which the softmax brings when it has read the last S of the one before.
+        Walker sw = walk;
+        Stretch ss;
+        int sj = 0, s_seg = -1, s_left = 0, seg = -1, it = 0;
+        bool more = true, ok = true;
+        auto s_step = [&]() {      // the next tile's S, if its stretch, Q and K are there
+            if (s_left == 0) {
+                if (!more || s_seg > seg) return;   // (one stretch ahead: its Q is the barrier's next phase)
+                more = sw.next(line, ss);
+                if (!more) return;
+                ++s_seg;
+                s_left = ss.t1 - ss.t0;
+            }
+            const int st = sj % S;
+            if (!__all_sync(0xffffffffu, mbar_test(q_full, (uint32_t)(s_seg & 1)) &&
+                                             mbar_test(&kv_full[st], (uint32_t)((sj / S) & 1))))
+                return;
+            tc_fence_after();
+            const uint32_t ka = smem_u32(ring + st * 2 * C::KV), d = tS + (sj & 1) * 64;
+            if (leader) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    tc_mma_bf16_ts(tS + (sj & 1) * 64, tQ + (s_seg & 1) * 64 + kk * 8,
-                                   umma_desc_sw128(ka + (kk >> 2) * 8192) + 2 * (kk & 3), IDESC_S, kk > 0 ? 1u : 0u);
+                    tc_mma_bf16_ts(d, tQ + kk * 8, umma_desc_sw128(ka + (kk >> 2) * 8192) + 2 * (kk & 3), IDESC_S,
+                                   kk > 0 ? 1u : 0u);
                 tc_commit(&s_full[sj & 1]);
-                ++sj;
-                --s_left;
-            };
-            while (ok && walk.next(line, s)) {
-                ++seg;
-                for (int t = s.t0; t < s.t1 && ok; ++t, ++it) {
-                    const int pb = it & 1;
-                    // whichever comes first: K of the next tile, or P of this one
-                    uint64_t since = 0;
-                    for (uint32_t n = 1;; ++n) {
-                        if (sj < it + 2) s_step();
-                        if (sj > it && mbar_test(&p_full[pb], (uint32_t)((it >> 1) & 1))) break;
-                        if ((n & 1023u) == 0) {
-                            const uint64_t now = globaltimer_ns();
-                            if (!since) since = now;
-                            if (!*abort_flag && now - since > kWaitLimitNs) {
-                                *abort_flag = 1;
-                                if (p.wait_status) atomicCAS(p.wait_status, 0, DFLASH_TIMEOUT);
-                            }
-                            if (*abort_flag) {
-                                ok = false;
-                                break;
-                            }
+            }
+            __syncwarp();
+            ++sj;
+            --s_left;
+        };
+        while (ok && walk.next(line, s)) {
+            ++seg;
+            for (int t = s.t0; t < s.t1 && ok; ++t, ++it) {
+                const int pb = it & 1;
+                // whichever comes first: K of the next tile, or P of this one
+                uint64_t since = 0;
+                for (uint32_t n = 1;; ++n) {
+                    if (sj < it + 2) s_step();
+                    if (sj > it && __all_sync(0xffffffffu, mbar_test(&p_full[pb], (uint32_t)((it >> 1) & 1)))) break;
+                    if ((n & 1023u) == 0) {
+                        const uint64_t now = globaltimer_ns();
+                        if (!since) since = now;
+                        if (!*abort_flag && now - since > kWaitLimitNs) {
+                            *abort_flag = 1;
+                            if (p.wait_status) atomicCAS(p.wait_status, 0, DFLASH_TIMEOUT);
+                        }
+                        if (__any_sync(0xffffffffu, *abort_flag)) {
+                            ok = false;
+                            break;
                         }
                     }
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t va = smem_u32(ring + ((it % S) * 2 + 1) * C::KV);
+                }
+                if (!ok) break;
+                tc_fence_after();
+                if (sj == it + 1) s_step();      // not there yet for some reason: the next tile first
+                s_step();
+                const uint32_t va = smem_u32(ring + ((it % S) * 2 + 1) * C::KV), d = tO + pb * 128, a = tP + pb * 32;
+                const uint32_t add = t >= s.t0 + 2 ? 1u : 0u;
+                if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        tc_mma_bf16_ts(tO + pb * 128, tS + pb * 64 + kk * 8,
-                                       umma_desc_sw128_mn(va + kk * 2048, 8192, 1024), IDESC_PV,
-                                       (t >= s.t0 + 2 || kk > 0) ? 1u : 0u);
+                        tc_mma_bf16_ts(d, a + kk * 8, umma_desc_sw128_mn(va + kk * 2048, 8192, 1024), IDESC_PV,
+                                       kk > 0 ? 1u : add);
                     tc_commit(&o_done[pb]);
                     tc_commit(&kv_empty[it % S]);
                 }
+                __syncwarp();
             }
-            if (*abort_flag) {
-                tc_commit(drain);   // the issued MMAs finish before the tensor memory is released
-                volatile int never = 0;
-                mbar_wait(drain, 0, &never, nullptr);
-            }
+        }
+        if (__any_sync(0xffffffffu, *abort_flag)) {
+            if (leader) tc_commit(drain);   // the issued MMAs finish before the tensor memory is released
+            __syncwarp();
+            volatile int never = 0;
+            mbar_wait(drain, 0, &never, nullptr);
         }
     } else {
         // ------------------------------------------------------------ softmax
@@ -236,9 +245,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
         const int row = rl % RW, cs = rl / RW;                 // vector of the tile, key slice (warp-uniform)
         const int e256 = tid - 64;
         const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
-        const uint32_t my_s = tS + lanes + w * 64, my_o = tO + lanes + w * 128;
-        // the lane's vector of stretch x into Q buffer b (zero past the tile's vectors); one group
-        auto put_q = [&](const Stretch& x, int b) {
+        const uint32_t my_s = tS + lanes + w * 64, my_p = tP + lanes + w * 32, my_o = tO + lanes + w * 128;
+        // the lane's vector of stretch x into the Q operand (zero past the tile's vectors)
+        auto put_q = [&](const Stretch& x) {
             const int4 e = line.ent[x.i];
             const bool have = row < (x.r1 - x.r0) * p.G;
             const __nv_bfloat16* src = (const __nv_bfloat16*)p.q + (size_t)(e.y + x.r0 + row / p.G) * p.q_stride +
@@ -258,23 +267,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                     v[4 * k + 2] = __uint_as_float(u.z);
                     v[4 * k + 3] = __uint_as_float(u.w);
                 }
-                tmem_st16(tQ + lanes + b * 64 + c0, v);
+                tmem_st16(tQ + lanes + c0, v);
             }
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&q_full[b]);
+            mbar_arrive(q_full);
         };
         Stretch nx;
         bool more = walk.next(line, nx);
-        if (more && w == 0) put_q(nx, 0);
-        int it0 = 0, seg = 0;             // tiles and stretches before this one
+        if constexpr (CS > 1) {           // the other slices' columns of this lane's P stay zero
+            const uint32_t z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+            for (int c0 = 0; c0 < 32; c0 += 8) tmem_st8u(my_p + c0, z);
+            tmem_wait_st();
+        }
+        if (more && w == 0) put_q(nx);
+        int it0 = 0;                      // tiles before this stretch
         bool ok = true;
         while (more && ok) {
             s = nx;
             more = walk.next(line, nx);
-            // the other Q buffer is free: S of all tiles before this stretch has been read
-            ++seg;
-            if (more && w == (seg & 1)) put_q(nx, seg & 1);
             const int4 e = line.ent[s.i];
             const int nvec = (s.r1 - s.r0) * p.G;
             const int pos = e.w + s.r0 + row / p.G;                    // this lane's position (padding lanes: any)
@@ -327,8 +339,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                 const float nb = floorf(fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
                                               fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * p.scale_log2);
                 const bool grow = nb > base + kBaseLag;
+                if (it >= 2) {   // the product of the group's tile before has read P and written O
+                    ok = mbar_wait(&o_done[w], (uint32_t)(((it - 2) >> 1) & 1), abort_flag, p.wait_status);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
                 if (__any_sync(0xffffffffu, grow)) {
-                    if (t >= s.t0 + 2) {   // O holds earlier tiles (their products ran before this S)
+                    if (t >= s.t0 + 2) {   // O holds earlier tiles
                         const float f = grow ? exp2f(base - nb) : 1.0f;
 #pragma unroll 1
                         for (int c0 = 0; c0 < D; c0 += 16) {
@@ -343,13 +361,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                     if (grow) base = nb;
                 }
                 const float bb = (base == -INFINITY) ? 0.f : base;
-                // P over S; with several slices the lane's other columns are zero
-                if constexpr (CS > 1) {
-                    const uint32_t z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-                    for (int c0 = 0; c0 < 32; c0 += 8)
-                        if (c0 / (KC / 2) != cs) tmem_st8u(my_s + c0, z);
-                }
                 float ls[KC / 16];
 #pragma unroll
                 for (int c0 = 0; c0 < KC; c0 += 16) {
@@ -363,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                         pk[i / 2] = pack_bf16(e0, e1);
                     }
                     ls[c0 >> 4] = s2;
-                    tmem_st8u(my_s + cs * (KC / 2) + c0 / 2, pk);
+                    tmem_st8u(my_p + cs * (KC / 2) + c0 / 2, pk);
                 }
 #pragma unroll
                 for (int i = 0; i < KC / 16; ++i) l += ls[i];
@@ -381,7 +392,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             // ---- the stretch's rows: group 1's O to shared memory, group 0 adds its own, then the
             // copies of a vector are added.  Bases differ by integers, so all factors are exact.
             ml[w * 128 + rl] = make_float2(base, l);
-            if (w == 1) {
+            if (w == 0) {
+                if (more) put_q(nx);      // every S of this stretch has been read
+            } else {
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
                     float v[32];
