@@ -14,8 +14,8 @@
 //              mask it where the tile has keys that some row does not see, write P =
 //              bf16(2^(t - b)), rescale O by an exact power of two when b moves.
 //   warp 0     TMA: K and V tiles of 64 keys, one box per page and 64-column half.
-//   warp 1     tcgen05.mma: once P of a tile is there, first S = Q K^T of the group's next tile
-//              (what its softmax waits for), then O += P V.
+//   warp 1     tcgen05.mma: S = Q K^T of a group's next tile once it has read the one before,
+//              O += P V once P is there.
 //
 // An item that several CTAs hold is joined by a second launch (k_paged_join): adding up to 18
 // partials of 32 KB took one CTA 15 us, all SMs together 2 us.
@@ -61,7 +61,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
     uint64_t* s_full = kv_empty + S;                                 // [2]
     uint64_t* p_full = s_full + 2;                                   // [2]
     uint64_t* o_done = p_full + 2;                                   // [2]
-    uint64_t* q_full = o_done + 2;
+    uint64_t* s_read = o_done + 2;                                   // [2]
+    uint64_t* q_full = s_read + 2;
     uint64_t* drain = q_full + 1;
     uint32_t* tmem_slot = (uint32_t*)(drain + 1);
     __shared__ int abort_s;
@@ -76,10 +77,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 128);
+            mbar_init(&s_read[i], 4);
+            mbar_init(&p_full[i], 4);
             mbar_init(&o_done[i], 1);
         }
-        mbar_init(q_full, 128);
+        mbar_init(q_full, 4);
         mbar_init(drain, 1);
         abort_s = 0;
         fence_mbar_init();
@@ -163,13 +165,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
         constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, true);
         const bool leader = elect_one();
         // S runs ahead on its own walk over the stretches.  S of tile j + 2 goes where S of tile j
-        // was, once the softmax has read that (P of tile j is there); the first S of a stretch
-        // waits for its Q, which the softmax brings when it has read the last S of the one before.
+        // was, as soon as the softmax has read that, so a group finds its next S waiting; the
+        // first S of a stretch waits for its Q, which the softmax brings when it has read the last
+        // S of the one before.
         Walker sw = walk;
         Stretch ss;
         int sj = 0, s_seg = -1, s_left = 0, seg = -1, it = 0;
         bool more = true, ok = true;
-        auto s_step = [&]() {      // the next tile's S, if its stretch, Q and K are there
+        auto s_step = [&]() {      // the next tile's S, if all that it needs is there
             if (s_left == 0) {
                 if (!more || s_seg > seg) return;   // (one stretch ahead: its Q is the barrier's next phase)
                 more = sw.next(line, ss);
@@ -178,8 +181,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                 s_left = ss.t1 - ss.t0;
             }
             const int st = sj % S;
-            if (!__all_sync(0xffffffffu, mbar_test(q_full, (uint32_t)(s_seg & 1)) &&
-                                             mbar_test(&kv_full[st], (uint32_t)((sj / S) & 1))))
+            if (!__all_sync(0xffffffffu, (sj < 2 || mbar_test(&s_read[sj & 1], (uint32_t)(((sj - 2) >> 1) & 1))) &&
+                                             mbar_test(&kv_full[st], (uint32_t)((sj / S) & 1)) &&
+                                             mbar_test(q_full, (uint32_t)(s_seg & 1))))
                 return;
             tc_fence_after();
             const uint32_t ka = smem_u32(ring + st * 2 * C::KV), d = tS + (sj & 1) * 64;
@@ -198,10 +202,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             ++seg;
             for (int t = s.t0; t < s.t1 && ok; ++t, ++it) {
                 const int pb = it & 1;
-                // whichever comes first: K of the next tile, or P of this one
                 uint64_t since = 0;
-                for (uint32_t n = 1;; ++n) {
-                    if (sj < it + 2) s_step();
+                for (uint32_t n = 1;; ++n) {      // whichever comes first: a next S, or P of this tile
+                    s_step();
                     if (sj > it && __all_sync(0xffffffffu, mbar_test(&p_full[pb], (uint32_t)((it >> 1) & 1)))) break;
                     if ((n & 1023u) == 0) {
                         const uint64_t now = globaltimer_ns();
@@ -218,8 +221,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                 }
                 if (!ok) break;
                 tc_fence_after();
-                if (sj == it + 1) s_step();      // not there yet for some reason: the next tile first
-                s_step();
                 const uint32_t va = smem_u32(ring + ((it % S) * 2 + 1) * C::KV), d = tO + pb * 128, a = tP + pb * 32;
                 const uint32_t add = t >= s.t0 + 2 ? 1u : 0u;
                 if (leader) {
@@ -271,7 +272,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             }
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(q_full);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
         };
         Stretch nx;
         bool more = walk.next(line, nx);
@@ -315,6 +317,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                 } else {
                     tmem_ld16w(my_s + cs * KC, x);
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_read[w]);
                 // tiles with keys that some row does not see
                 if (k0 + 64 > hi_all || (k0 < lo_all && k0 + 64 > p.sinks)) {
 #pragma unroll
@@ -380,7 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                 for (int i = 0; i < KC / 16; ++i) l += ls[i];
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&p_full[w]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[w]);
             }
             if (ok && last >= 0)
                 ok = mbar_wait(&o_done[w], (uint32_t)((last >> 1) & 1), abort_flag, p.wait_status);
