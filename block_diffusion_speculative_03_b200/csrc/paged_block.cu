@@ -14,8 +14,9 @@
 //              mask it where the tile has keys that some row does not see, write P =
 //              bf16(2^(t - b)), rescale O by an exact power of two when b moves.
 //   warp 0     TMA: K and V tiles of 64 keys, one box per page and 64-column half.
-//   warp 1     tcgen05.mma: S = Q K^T of a group's next tile once it has read the one before,
-//              O += P V once P is there.
+//   warp 1     tcgen05.mma: S = Q K^T of a group's next tile once it has read the one before.
+//   warp 10    tcgen05.mma: O += P V once P is there.  (Two issuers that each wait for one thing:
+//              one that polled for both took 300 to 700 cycles to notice either.)
 //
 // An item that several CTAs hold is joined by a second launch (k_paged_join): adding up to 18
 // partials of 32 KB took one CTA 15 us, all SMs together 2 us.
@@ -27,7 +28,7 @@ namespace df {
 
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr int kSoftmax = 256;    // threads of the two softmax groups
 constexpr float kBaseLag = 8.0f;
 constexpr int kOverhead = 4;   // units that starting and ending an item costs, in tiles
@@ -39,7 +40,8 @@ template <int D> struct BlockCfg {
     static constexpr int STAGES = D == 128 ? 4 : 8;
     static constexpr int RING = STAGES * 2 * KV;
     static constexpr int OLD = D + 4;
-    static constexpr int JOIN = 128 * OLD * 4;
+    static constexpr int HLD = D / 2 + 4;
+    static constexpr int JOIN = 256 * HLD * 4;               // >= 128 * OLD * 4
     static constexpr int SMEM = 1024 + RING + JOIN + 2 * 128 * 8 + kLineBytes + 512;
     static constexpr int SLOT = 128 * (D + 2);               // floats of a partial
     // tensor memory columns: S[2] (64 each), P[2] (32 bf16 pairs each), Q (D / 2), O[2] (D each)
@@ -63,8 +65,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
     uint64_t* o_done = p_full + 2;                                   // [2]
     uint64_t* s_read = o_done + 2;                                   // [2]
     uint64_t* q_full = s_read + 2;
-    uint64_t* drain = q_full + 1;
-    uint32_t* tmem_slot = (uint32_t*)(drain + 1);
+    uint64_t* q_free = q_full + 1;
+    uint64_t* drain = q_free + 1;                                    // [2]
+    uint32_t* tmem_slot = (uint32_t*)(drain + 2);
     __shared__ int abort_s;
     __shared__ long long sums[kThreads / 32];
     volatile int* abort_flag = &abort_s;
@@ -80,9 +83,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             mbar_init(&s_read[i], 4);
             mbar_init(&p_full[i], 4);
             mbar_init(&o_done[i], 1);
+            mbar_init(&drain[i], 1);
         }
         mbar_init(q_full, 4);
-        mbar_init(drain, 1);
+        mbar_init(q_free, 8);
         abort_s = 0;
         fence_mbar_init();
         tma_prefetch_desc(&p.tmap_half);
@@ -157,68 +161,52 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             for (int k = max(0, it - S); k < it; ++k) mbar_wait(&kv_full[k % S], (uint32_t)((k / S) & 1), &never, nullptr);
         }
     } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
+        // ------------------------------------------------------------ S = Q K^T
         // The whole warp walks and waits, one elected lane issues: in code that the warp runs
         // together the operands stay in uniform registers (128 x 64 x 16 measured 33 cycles an
-        // instruction against 47-70 in a branch of one lane).
+        // instruction against 47-70 in a branch of one lane).  S of tile j + 2 goes where S of
+        // tile j was, as soon as the softmax has read that, so a group finds its next S waiting.
         constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 64);
+        const bool leader = elect_one();
+        int it = 0, seg = 0;
+        bool ok = true;
+        for (; ok && walk.next(line, s); ++seg) {
+            ok = __all_sync(0xffffffffu, mbar_wait(q_full, (uint32_t)(seg & 1), abort_flag, p.wait_status));
+            for (int t = s.t0; t < s.t1 && ok; ++t, ++it) {
+                const int st = it % S;
+                ok = mbar_wait(&kv_full[st], (uint32_t)((it / S) & 1), abort_flag, p.wait_status);
+                if (ok && it >= 2) ok = mbar_wait(&s_read[it & 1], (uint32_t)(((it - 2) >> 1) & 1), abort_flag, p.wait_status);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t ka = smem_u32(ring + st * 2 * C::KV), d = tS + (it & 1) * 64;
+                if (leader) {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        tc_mma_bf16_ts(d, tQ + kk * 8, umma_desc_sw128(ka + (kk >> 2) * 8192) + 2 * (kk & 3), IDESC_S,
+                                       kk > 0 ? 1u : 0u);
+                    tc_commit(&s_full[it & 1]);
+                }
+                __syncwarp();
+            }
+        }
+        if (__any_sync(0xffffffffu, *abort_flag)) {
+            if (leader) tc_commit(&drain[0]);   // the issued MMAs finish before the tensor memory is released
+            __syncwarp();
+            volatile int never = 0;
+            mbar_wait(&drain[0], 0, &never, nullptr);
+        }
+    } else if (warp == 10) {
+        // ------------------------------------------------------------ O += P V
         constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, true);
         const bool leader = elect_one();
-        // S runs ahead on its own walk over the stretches.  S of tile j + 2 goes where S of tile j
-        // was, as soon as the softmax has read that, so a group finds its next S waiting; the
-        // first S of a stretch waits for its Q, which the softmax brings when it has read the last
-        // S of the one before.
-        Walker sw = walk;
-        Stretch ss;
-        int sj = 0, s_seg = -1, s_left = 0, seg = -1, it = 0;
-        bool more = true, ok = true;
-        auto s_step = [&]() {      // the next tile's S, if all that it needs is there
-            if (s_left == 0) {
-                if (!more || s_seg > seg) return;   // (one stretch ahead: its Q is the barrier's next phase)
-                more = sw.next(line, ss);
-                if (!more) return;
-                ++s_seg;
-                s_left = ss.t1 - ss.t0;
-            }
-            const int st = sj % S;
-            if (!__all_sync(0xffffffffu, (sj < 2 || mbar_test(&s_read[sj & 1], (uint32_t)(((sj - 2) >> 1) & 1))) &&
-                                             mbar_test(&kv_full[st], (uint32_t)((sj / S) & 1)) &&
-                                             mbar_test(q_full, (uint32_t)(s_seg & 1))))
-                return;
-            tc_fence_after();
-            const uint32_t ka = smem_u32(ring + st * 2 * C::KV), d = tS + (sj & 1) * 64;
-            if (leader) {
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    tc_mma_bf16_ts(d, tQ + kk * 8, umma_desc_sw128(ka + (kk >> 2) * 8192) + 2 * (kk & 3), IDESC_S,
-                                   kk > 0 ? 1u : 0u);
-                tc_commit(&s_full[sj & 1]);
-            }
-            __syncwarp();
-            ++sj;
-            --s_left;
-        };
+        int it = 0;
+        bool ok = true;
         while (ok && walk.next(line, s)) {
-            ++seg;
-            for (int t = s.t0; t < s.t1 && ok; ++t, ++it) {
+            for (int t = s.t0; t < s.t1; ++t, ++it) {
                 const int pb = it & 1;
-                uint64_t since = 0;
-                for (uint32_t n = 1;; ++n) {      // whichever comes first: a next S, or P of this tile
-                    s_step();
-                    if (sj > it && __all_sync(0xffffffffu, mbar_test(&p_full[pb], (uint32_t)((it >> 1) & 1)))) break;
-                    if ((n & 1023u) == 0) {
-                        const uint64_t now = globaltimer_ns();
-                        if (!since) since = now;
-                        if (!*abort_flag && now - since > kWaitLimitNs) {
-                            *abort_flag = 1;
-                            if (p.wait_status) atomicCAS(p.wait_status, 0, DFLASH_TIMEOUT);
-                        }
-                        if (__any_sync(0xffffffffu, *abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                    }
-                }
+                ok = mbar_wait(&p_full[pb], (uint32_t)((it >> 1) & 1), abort_flag, p.wait_status);
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t va = smem_u32(ring + ((it % S) * 2 + 1) * C::KV), d = tO + pb * 128, a = tP + pb * 32;
@@ -229,16 +217,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                         tc_mma_bf16_ts(d, a + kk * 8, umma_desc_sw128_mn(va + kk * 2048, 8192, 1024), IDESC_PV,
                                        kk > 0 ? 1u : add);
                     tc_commit(&o_done[pb]);
-                    tc_commit(&kv_empty[it % S]);
+                    tc_commit(&kv_empty[it % S]);      // S of this tile was done before its P
                 }
                 __syncwarp();
             }
         }
         if (__any_sync(0xffffffffu, *abort_flag)) {
-            if (leader) tc_commit(drain);   // the issued MMAs finish before the tensor memory is released
+            if (leader) tc_commit(&drain[1]);
             __syncwarp();
             volatile int never = 0;
-            mbar_wait(drain, 0, &never, nullptr);
+            mbar_wait(&drain[1], 0, &never, nullptr);
         }
     } else {
         // ------------------------------------------------------------ softmax
@@ -284,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             tmem_wait_st();
         }
         if (more && w == 0) put_q(nx);
-        int it0 = 0;                      // tiles before this stretch
+        int it0 = 0, seg = 0;             // tiles and stretches before this one
         bool ok = true;
         while (more && ok) {
             s = nx;
@@ -307,6 +295,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
+                // the product of the group's tile before has read P and written O (looked at early,
+                // waited for where it matters)
+                const bool o_ready = it < 2 || mbar_test(&o_done[w], (uint32_t)(((it - 2) >> 1) & 1));
                 const int k0 = s.span.tile(t) * 64, kvb = k0 + cs * KC;
                 float x[KC];
                 if constexpr (KC == 64) {
@@ -344,12 +335,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                 const float nb = floorf(fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
                                               fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * p.scale_log2);
                 const bool grow = nb > base + kBaseLag;
-                if (it >= 2) {   // the product of the group's tile before has read P and written O
+                if (!__all_sync(0xffffffffu, o_ready)) {
                     ok = mbar_wait(&o_done[w], (uint32_t)(((it - 2) >> 1) & 1), abort_flag, p.wait_status);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    tc_fence_after();
                 }
+                tc_fence_after();
                 if (__any_sync(0xffffffffu, grow)) {
                     if (t >= s.t0 + 2) {   // O holds earlier tiles
                         const float f = grow ? exp2f(base - nb) : 1.0f;
@@ -388,54 +379,113 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[w]);
             }
+            // this warp has read its last S of the stretch; when all have, Q may change
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_free);
+            if (ok && more && w == 0) {
+                ok = mbar_wait(q_free, (uint32_t)(seg & 1), abort_flag, p.wait_status);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok) put_q(nx);
+            }
+            ++seg;
             if (ok && last >= 0)
                 ok = mbar_wait(&o_done[w], (uint32_t)((last >> 1) & 1), abort_flag, p.wait_status);
+            ml[w * 128 + rl] = make_float2(base, l);
             if (named_bar_or(1, kSoftmax, !ok)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            // ---- the stretch's rows: group 1's O to shared memory, group 0 adds its own, then the
-            // copies of a vector are added.  Bases differ by integers, so all factors are exact.
-            ml[w * 128 + rl] = make_float2(base, l);
-            if (w == 0) {
-                if (more) put_q(nx);      // every S of this stretch has been read
-            } else {
-#pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
-                    float v[32];
-                    tmem_ld32w(my_o + c0, v);
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        *reinterpret_cast<float4*>(join + rl * C::OLD + c0 + i) =
-                            last >= 0 ? make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
-                }
-            }
-            named_bar_sync(1, kSoftmax);
-            if (w == 0) {
-                const float2 other = ml[128 + rl];
-                const float B = fmaxf(base, other.x), z = B == -INFINITY ? 0.f : B;
-                const float f0 = exp2f(base - z), f1 = exp2f(other.x - z);
-#pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
-                    float v[32];
-                    tmem_ld32w(my_o + c0, v);
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        float4* d4 = reinterpret_cast<float4*>(join + rl * C::OLD + c0 + i);
-                        float4 o = *d4;
-                        o.x = (last >= 0 ? f0 * v[i] : 0.f) + f1 * o.x;
-                        o.y = (last >= 0 ? f0 * v[i + 1] : 0.f) + f1 * o.y;
-                        o.z = (last >= 0 ? f0 * v[i + 2] : 0.f) + f1 * o.z;
-                        o.w = (last >= 0 ? f0 * v[i + 3] : 0.f) + f1 * o.w;
-                        *d4 = o;
-                    }
-                }
-                ml[rl] = make_float2(B, f0 * l + f1 * other.y);
-            }
-            named_bar_sync(1, kSoftmax);
+            // ---- the stretch's rows: the groups' O are added, then the copies of a vector.  Bases
+            // differ by integers, so all factors are exact powers of two.
             const bool whole = s.whole(), head = s.t0 == 0;   // head: holds the item's first tile
             float* slot = p.partial + (size_t)(2 * blockIdx.x + (head ? 1 : 0)) * C::SLOT;
+            if constexpr (CS == 1) {
+                // each group finishes half the columns: it gives the other half away
+                const float2 other = ml[(w ^ 1) * 128 + rl];
+                const float B = fmaxf(base, other.x), z = B == -INFINITY ? 0.f : B;
+                const float f0 = last >= 0 ? exp2f(base - z) : 0.f, f1 = exp2f(other.x - z);
+                const float L = f0 * l + f1 * other.y, inv = L == 0.f ? 0.f : 1.0f / L;
+                float* mine = join + (w * 128 + rl) * C::HLD;
+                const float* theirs = join + ((w ^ 1) * 128 + rl) * C::HLD;
+                const uint32_t keep = my_o + w * (D / 2), give = my_o + (w ^ 1) * (D / 2);
+#pragma unroll
+                for (int c0 = 0; c0 < D / 2; c0 += 32) {
+                    float v[32];
+                    tmem_ld32w(give + c0, v);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<float4*>(mine + c0 + i) =
+                            last >= 0 ? make_float4(f0 * v[i], f0 * v[i + 1], f0 * v[i + 2], f0 * v[i + 3])
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+                named_bar_sync(1, kSoftmax);
+                __nv_bfloat16* dst = (__nv_bfloat16*)p.out +
+                                     ((size_t)(e.y + s.r0 + row / p.G) * p.nq + (size_t)s.g * p.G + row % p.G) * D + w * (D / 2);
+                float* part = slot + 256 + row * D + w * (D / 2);
+#pragma unroll
+                for (int c0 = 0; c0 < D / 2; c0 += 32) {
+                    float v[32];
+                    tmem_ld32w(keep + c0, v);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 o = *reinterpret_cast<const float4*>(theirs + c0 + i);
+                        v[i] = (last >= 0 ? f0 * v[i] : 0.f) + o.x;
+                        v[i + 1] = (last >= 0 ? f0 * v[i + 1] : 0.f) + o.y;
+                        v[i + 2] = (last >= 0 ? f0 * v[i + 2] : 0.f) + o.z;
+                        v[i + 3] = (last >= 0 ? f0 * v[i + 3] : 0.f) + o.w;
+                    }
+                    if (row < nvec) {
+                        if (whole) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 8)
+                                *reinterpret_cast<uint4*>(dst + c0 + i) =
+                                    make_uint4(pack_bf16(v[i] * inv, v[i + 1] * inv), pack_bf16(v[i + 2] * inv, v[i + 3] * inv),
+                                               pack_bf16(v[i + 4] * inv, v[i + 5] * inv), pack_bf16(v[i + 6] * inv, v[i + 7] * inv));
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4)
+                                *reinterpret_cast<float4*>(part + c0 + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                        }
+                    }
+                }
+                if (!whole && w == 0 && row < nvec) *reinterpret_cast<float2*>(slot + 2 * row) = make_float2(B, L);
+            } else {
+                // group 1's O to shared memory, group 0 adds its own
+                if (w == 1) {
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        float v[32];
+                        tmem_ld32w(my_o + c0, v);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<float4*>(join + rl * C::OLD + c0 + i) =
+                                last >= 0 ? make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                }
+                named_bar_sync(1, kSoftmax);
+                if (w == 0) {
+                    const float2 other = ml[128 + rl];
+                    const float B = fmaxf(base, other.x), z = B == -INFINITY ? 0.f : B;
+                    const float f0 = exp2f(base - z), f1 = exp2f(other.x - z);
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        float v[32];
+                        tmem_ld32w(my_o + c0, v);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            float4* d4 = reinterpret_cast<float4*>(join + rl * C::OLD + c0 + i);
+                            float4 o = *d4;
+                            o.x = (last >= 0 ? f0 * v[i] : 0.f) + f1 * o.x;
+                            o.y = (last >= 0 ? f0 * v[i + 1] : 0.f) + f1 * o.y;
+                            o.z = (last >= 0 ? f0 * v[i + 2] : 0.f) + f1 * o.z;
+                            o.w = (last >= 0 ? f0 * v[i + 3] : 0.f) + f1 * o.w;
+                            *d4 = o;
+                        }
+                    }
+                    ml[rl] = make_float2(B, f0 * l + f1 * other.y);
+                }
+                named_bar_sync(1, kSoftmax);
             for (int i = e256; i < nvec * (D / 8); i += kSoftmax) {
                 const int v = i / (D / 8), c = (i % (D / 8)) * 8;
                 float B = -INFINITY, L = 0.f, a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -464,6 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                     *reinterpret_cast<float4*>(slot + 256 + v * D + c + 4) = make_float4(a[4], a[5], a[6], a[7]);
                     if (c == 0) *reinterpret_cast<float2*>(slot + 2 * v) = make_float2(B, L);
                 }
+            }
             }
             if (!whole && head && e256 == 0) {
                 rec[0] = make_int4(line_owner(s.v0 + kOverhead + s.span.nt - 1, U, P), nvec, e.y + s.r0, s.g);
