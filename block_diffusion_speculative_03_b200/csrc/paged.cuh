@@ -78,6 +78,7 @@ struct PagedAttnParams {
     int uniform;             // rows per entry when row_start is null
     int total_rows, max_rows, row_tiles;
     int rt;                  // positions per row tile: query rows of a tile = rt * G
+    int g_magic;             // v / G = v * g_magic >> 16 for v < 512 (set by the launchers)
     int G, nq, nkv;
     int causal, window, sinks;
     // slab rows (units of one head's row): page (or request), kind and kv-head strides, the layer's first row
@@ -163,27 +164,38 @@ DF_DEV bool key_visible(int k, int pos, int hi, int window, int sinks) {
 // ---------------------------------------------------------------------------
 constexpr int kLineTile = 64;     // keys of a tile
 
-// Shared memory of a CTA: the entries and the units before each.
+// A row's integer base b moves when the floor of its running maximum passes b + kBaseLag, to
+// kBaseLead above it: P stays below 2^(kBaseLag + 1), and after its first tile a row's scores
+// have to rise by 2^16 before O is rescaled again (with the base at the maximum itself, rows
+// whose first tile shows only a few sinks rescaled in most tiles, 700 cycles each time).  A
+// weight that vanishes for the lead is below 2^-118 of the row's largest.
+constexpr float kBaseLag = 8.0f, kBaseLead = 8.0f;
+
+// Shared memory of a CTA: the entries and the units before each.  Units are 32-bit (2^31 of them
+// are two hours of work for a whole device; a call with more records DFLASH_UNSUPPORTED).
 struct Line {
     int4* ent;          // [n]: sequence, first row, rows (0: nothing to do), length
-    long long* pre;     // [n + 1], per kv head
+    int* pre;           // [n + 1]
     int n, rt, ovh, nkv, causal, window, sinks;
 
-    DF_DEV int row_tiles(int i) const { return (ent[i].z + rt - 1) / rt; }
+    DF_DEV int row_tiles(int i) const {
+        const int z = ent[i].z;
+        return z <= rt ? (z > 0) : (z + rt - 1) / rt;
+    }
     DF_DEV KeySpan span(const int4& e, int t) const {
         const int r0 = t * rt, r1 = min(e.z, r0 + rt);
         return key_span(e.w, e.z, r0, r1, causal, window, sinks, kLineTile);
     }
 };
-constexpr int kLineBytes = kPoolMaxSeqs * 16 + (kPoolMaxSeqs + 2) * 8;
+constexpr int kLineBytes = kPoolMaxSeqs * 16 + (kPoolMaxSeqs + 4) * 4;
 
 // Fill the line (the whole block; sums: THREADS / 32 long longs of shared memory).  Rows of
-// bad entries are zeroed, each entry by one CTA.  Returns U.
+// bad entries are zeroed, each entry by one CTA.  Returns U, 0 when there is nothing to do.
 template <int THREADS, int D>
-DF_DEV long long line_plan(const PagedAttnParams& p, Line& L, uint8_t* mem, long long* sums, int ovh) {
+DF_DEV int line_plan(const PagedAttnParams& p, Line& L, uint8_t* mem, long long* sums, int ovh) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     L.ent = (int4*)mem;
-    L.pre = (long long*)(mem + kPoolMaxSeqs * 16);
+    L.pre = (int*)(mem + kPoolMaxSeqs * 16);
     L.n = p.n;
     L.rt = p.rt;
     L.ovh = ovh;
@@ -191,6 +203,8 @@ DF_DEV long long line_plan(const PagedAttnParams& p, Line& L, uint8_t* mem, long
     L.causal = p.causal;
     L.window = p.window;
     L.sinks = p.sinks;
+    long long w = 0;              // units of entry tid, in the one-row-tile case of the first THREADS entries
+    const bool quick = p.n <= 32 && p.row_tiles == 1;      // one warp scans
     for (int i = tid; i < p.n; i += THREADS) {
         AttnEntry e = attn_entry(p, i);
         if (e.bad) {
@@ -203,26 +217,47 @@ DF_DEV long long line_plan(const PagedAttnParams& p, Line& L, uint8_t* mem, long
             e.count = 0;
         }
         L.ent[i] = make_int4(e.seq, e.start, e.count, e.len);
-        if (p.row_tiles == 1) L.pre[i] = e.count > 0 ? L.span(L.ent[i], 0).nt + ovh : 0;
+        if (p.row_tiles == 1) {
+            w = e.count > 0 ? (long long)(L.span(L.ent[i], 0).nt + ovh) * p.nkv : 0;
+            L.pre[i] = (int)min(w, 0x7fffffffll);
+        }
+    }
+    if (quick) {
+        if (warp == 0) {
+            long long inc = w;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += u;
+            }
+            if (lane < p.n) L.pre[lane] = (int)min(inc - w, 0x7fffffffll);
+            if (lane == p.n - 1) sums[0] = inc;
+        }
+        __syncthreads();
+        const long long all = sums[0];
+        if (tid == 0) L.pre[p.n] = (int)min(all, 0x7fffffffll);
+        __syncthreads();
+        if (all >= 0x7fffffffll && tid == 0 && p.wait_status) set_error(p.wait_status, DFLASH_UNSUPPORTED);
+        return all < 0x7fffffffll ? (int)all : 0;
     }
     __syncthreads();
     if (p.row_tiles > 1) {
         for (int i = warp; i < p.n; i += THREADS / 32) {
             const int4 e = L.ent[i];
             const int T = L.row_tiles(i);
-            long long w = 0;
-            for (int t = lane; t < T; t += 32) w += L.span(e, t).nt + ovh;
+            long long x = 0;
+            for (int t = lane; t < T; t += 32) x += L.span(e, t).nt + ovh;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-            if (lane == 0) L.pre[i] = w;
+            for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            if (lane == 0) L.pre[i] = (int)min(x * p.nkv, 0x7fffffffll);
         }
         __syncthreads();
     }
     long long run = 0;
     for (int base = 0; base < p.n; base += THREADS) {
         const int i = base + tid;
-        const long long w = i < p.n ? L.pre[i] : 0;
-        long long inc = w;
+        const long long x = i < p.n ? L.pre[i] : 0;
+        long long inc = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long u = __shfl_up_sync(0xffffffffu, inc, o);
@@ -235,76 +270,85 @@ DF_DEV long long line_plan(const PagedAttnParams& p, Line& L, uint8_t* mem, long
             if (k < warp) before += sums[k];
             run += sums[k];
         }
-        if (i < p.n) L.pre[i] = before + inc - w;
+        if (i < p.n) L.pre[i] = (int)min(before + inc - x, 0x7fffffffll);
         __syncthreads();
     }
-    if (tid == 0) L.pre[p.n] = run;
+    if (tid == 0) L.pre[p.n] = (int)min(run, 0x7fffffffll);
     __syncthreads();
-    return run * p.nkv;
+    if (run >= 0x7fffffffll && tid == 0 && p.wait_status) set_error(p.wait_status, DFLASH_UNSUPPORTED);
+    return run < 0x7fffffffll ? (int)run : 0;
 }
 
 // A CTA's stretch of one item: key tiles [t0, t1) of span.nt for rows [r0, r1) of entry i.
 struct Stretch {
     int i, g, r0, r1, t0, t1;
     KeySpan span;
-    long long v0;       // the item's first unit
+    int v0;             // the item's first unit
     DF_DEV bool whole() const { return t0 == 0 && t1 == span.nt; }
 };
 struct Walker {
-    long long v, end;   // units still to come
+    int v, end;         // units still to come
     int i, t, g, off;   // item and units of it that lie before v
+    int T;              // row tiles of entry i
 
     // The calling warp as a whole; v < end <= U.
-    DF_DEV void start(const Line& L, long long begin, long long end_) {
+    DF_DEV void start(const Line& L, int begin, int end_) {
         v = begin;
         end = end_;
-        int lo = 0;
-        for (int hi = L.n; hi - lo > 1;) {
-            const int mid = (lo + hi) >> 1;
-            if (L.pre[mid] * L.nkv <= v) lo = mid;
-            else hi = mid;
+        const int lane = threadIdx.x & 31;
+        if (L.n <= 32) {      // entries without units share their start: the last that starts at or before v
+            const int x = lane < L.n ? L.pre[lane] : 0x7fffffff;
+            i = 31 - __clz(__ballot_sync(0xffffffffu, x <= v));
+        } else {
+            int lo = 0;
+            for (int hi = L.n; hi - lo > 1;) {
+                const int mid = (lo + hi) >> 1;
+                if (L.pre[mid] <= v) lo = mid;
+                else hi = mid;
+            }
+            i = lo;
+            while (L.pre[i + 1] <= v) ++i;
         }
-        i = lo;
-        while (L.pre[i + 1] * L.nkv <= v) ++i;     // entries without units share their start
-        long long local = v - L.pre[i] * L.nkv;
+        int local = v - L.pre[i];
         const int4 e = L.ent[i];
-        const int T = L.row_tiles(i), lane = threadIdx.x & 31;
+        T = L.row_tiles(i);
         t = 0;
+        int size = L.span(e, 0).nt + L.ovh;
         if (T > 1) {
             for (int tb = 0;; tb += 32) {
                 const int tt = tb + lane;
-                const long long w = tt < T ? (long long)(L.span(e, tt).nt + L.ovh) * L.nkv : 0;
-                long long inc = w;
+                const int sz = tt < T ? L.span(e, tt).nt + L.ovh : 0;
+                int inc = sz * L.nkv;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+                    const int u = __shfl_up_sync(0xffffffffu, inc, o);
                     if (lane >= o) inc += u;
                 }
                 const unsigned m = __ballot_sync(0xffffffffu, inc > local);
                 if (m) {
                     const int src = __ffs(m) - 1;
                     t = tb + src;
-                    local -= __shfl_sync(0xffffffffu, inc - w, src);
+                    size = __shfl_sync(0xffffffffu, sz, src);
+                    local -= __shfl_sync(0xffffffffu, inc, src) - size * L.nkv;
                     break;
                 }
                 local -= __shfl_sync(0xffffffffu, inc, 31);
             }
         }
-        const int size = L.span(e, t).nt + L.ovh;
-        g = (int)(local / size);
-        off = (int)(local % size);
+        g = local / size;
+        off = local - g * size;
     }
     // The next stretch with tiles; false when the share is done.
     DF_DEV bool next(const Line& L, Stretch& s) {
         while (v < end) {
             const int4 e = L.ent[i];
-            s.span = L.span(e, t);
-            const int size = s.span.nt + L.ovh;
-            const int take = (int)min((long long)(size - off), end - v);
-            s.i = i;
-            s.g = g;
             s.r0 = t * L.rt;
             s.r1 = min(e.z, s.r0 + L.rt);
+            s.span = key_span(e.w, e.z, s.r0, s.r1, L.causal, L.window, L.sinks, kLineTile);
+            const int size = s.span.nt + L.ovh;
+            const int take = min(size - off, end - v);
+            s.i = i;
+            s.g = g;
             s.t0 = max(0, off - L.ovh);
             s.t1 = max(0, off + take - L.ovh);
             s.v0 = v - off;
@@ -314,9 +358,10 @@ struct Walker {
                 off = 0;
                 if (++g == L.nkv) {
                     g = 0;
-                    if (++t >= L.row_tiles(i)) {
+                    if (++t >= T) {
                         t = 0;
                         while (++i < L.n && L.ent[i].z == 0) {}
+                        if (i < L.n) T = L.row_tiles(i);
                     }
                 }
             }
@@ -325,6 +370,27 @@ struct Walker {
         return false;
     }
 };
+
+// Bounded wait on an mbarrier phase, as mbar_wait, for waits that are short and many: the
+// clock is first read after 64 tries (reading %globaltimer costs some 300 cycles, which every
+// wait that did not succeed at once paid otherwise).
+DF_DEV bool mbar_wait_short(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) == 0) {
+            if (*abort_flag) return false;
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kWaitLimitNs) {
+                *abort_flag = 1;
+                if (status) atomicCAS(status, 0, DFLASH_TIMEOUT);
+                return false;
+            }
+        }
+    }
+}
+
 // True for one lane of a converged warp, the same one every time.
 DF_DEV bool elect_one() {
     uint32_t r;
@@ -347,8 +413,21 @@ DF_DEV bool mbar_test(uint64_t* bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// 32 lanes x 64 consecutive 32-bit columns of tensor memory, waited for in the same statement.
+DF_DEV void tmem_ld64w(uint32_t taddr, float* v) {
+    uint32_t r[64];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
 // CTA that holds unit u.
-DF_DEV int line_owner(long long u, long long U, int P) { return (int)(((u + 1) * P - 1) / U); }
+DF_DEV int line_owner(int u, int U, int P) { return (int)((((long long)u + 1) * P - 1) / U); }
+DF_DEV int line_begin(int c, int U, int P) { return (int)((long long)c * U / P); }
 
 // Issue the TMA loads of one 64-key tile of K and V by a whole warp: pages looked up 32 at
 // a time.  A box is min(page_size, 64) rows; boxes in which no row sees a key are not loaded.

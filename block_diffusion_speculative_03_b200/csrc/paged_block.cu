@@ -9,11 +9,11 @@
 //
 //   warps 2-9  softmax, two groups of four warps that take the tiles in turn, each with its
 //              own S and O in tensor memory and its own running base and sum per lane (they are
-//              joined once per stretch: two chains hide each other's latencies, and nothing is
-//              exchanged between warps inside a stretch).  Per tile: read the lane's slice of S,
+//              joined once per stretch; the chains hide each other's latencies).  Per tile: read S,
 //              mask it where the tile has keys that some row does not see, write P =
 //              bf16(2^(t - b)), rescale O by an exact power of two when b moves.
-//   warp 0     TMA: K and V tiles of 64 keys, one box per page and 64-column half.
+//   warp 0, 11 TMA: K and V tiles of 64 keys, one box per page and 64-column half; warp 0 also
+//              stages the next stretch's Q.
 //   warp 1     tcgen05.mma: S = Q K^T of a group's next tile once it has read the one before.
 //   warp 10    tcgen05.mma: O += P V once P is there.  (Two issuers that each wait for one thing:
 //              one that polled for both took 300 to 700 cycles to notice either.)
@@ -28,25 +28,35 @@ namespace df {
 
 namespace {
 
-constexpr int kThreads = 352;
-constexpr int kSoftmax = 256;    // threads of the two softmax groups
-constexpr float kBaseLag = 8.0f;
 constexpr int kOverhead = 4;   // units that starting and ending an item costs, in tiles
 constexpr int kMinShare = 8;   // smallest share of a CTA, in units
+
+constexpr int kThreads = 384;
+constexpr int kSoftmax = 256;    // threads of the two softmax groups
+constexpr int kPvWarp = 10;
 
 template <int D> struct BlockCfg {
     static constexpr int HALVES = D / 64;
     static constexpr int KV = HALVES * 64 * 128;             // bytes of a K (or V) tile
-    static constexpr int STAGES = D == 128 ? 4 : 8;
+    static constexpr int STAGES = D == 128 ? 3 : 6;          // of K and of V
     static constexpr int RING = STAGES * 2 * KV;
     static constexpr int OLD = D + 4;
     static constexpr int HLD = D / 2 + 4;
     static constexpr int JOIN = 256 * HLD * 4;               // >= 128 * OLD * 4
-    static constexpr int SMEM = 1024 + RING + JOIN + 2 * 128 * 8 + kLineBytes + 512;
+    static constexpr int QLD = D * 2 + 16;                   // bytes of a staged Q vector: 16 more, so that lanes hit all banks
+    static constexpr int SMEM = 1024 + RING + JOIN + 2 * 128 * 8 + 128 * QLD + kLineBytes + 512;
+    static_assert(SMEM <= 227 * 1024, "shared memory");
     static constexpr int SLOT = 128 * (D + 2);               // floats of a partial
     // tensor memory columns: S[2] (64 each), P[2] (32 bf16 pairs each), Q (D / 2), O[2] (D each)
     static constexpr uint32_t T_S = 0, T_P = 128, T_Q = 192, T_O = 256, COLS = 512;
 };
+
+// The lowest n bits (n below 0: none, above 32: all).
+DF_DEV uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+// Floats of a partial: (base, sum) of the 128 vectors, then o, four columns of all vectors after
+// one another (a warp's lanes hold consecutive vectors: whole lines per store).
+DF_DEV int part_at(int v, int c) { return 256 + ((c >> 2) * 128 + v) * 4 + (c & 3); }
 
 template <int D, int CS>
 __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_constant__ PagedAttnParams p) {
@@ -54,19 +64,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
     constexpr int S = C::STAGES;
     constexpr int RW = 128 / CS, KC = 64 / CS;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* ring = smem_align_up<uint8_t>(smem_raw, 1024);          // [S][K, V]
+    uint8_t* ring = smem_align_up<uint8_t>(smem_raw, 1024);          // K [S], V [S]
     float* join = (float*)(ring + C::RING);                          // [128][OLD]
     float2* ml = (float2*)(ring + C::RING + C::JOIN);                // [2][128] base and sum per group and lane
-    uint8_t* line_mem = (uint8_t*)(ml + 256);
-    uint64_t* kv_full = (uint64_t*)(line_mem + kLineBytes);          // [S]
-    uint64_t* kv_empty = kv_full + S;                                // [S]
-    uint64_t* s_full = kv_empty + S;                                 // [2]
+    uint8_t* q_stage = (uint8_t*)(ml + 256);                         // [128][QLD] the next stretch's Q
+    uint8_t* line_mem = q_stage + 128 * C::QLD;
+    uint64_t* kv_full = (uint64_t*)(line_mem + kLineBytes);          // [2][S]: K, V
+    uint64_t* kv_empty = kv_full + 2 * S;                            // [2][S]
+    uint64_t* s_full = kv_empty + 2 * S;                             // [2]
     uint64_t* p_full = s_full + 2;                                   // [2]
     uint64_t* o_done = p_full + 2;                                   // [2]
     uint64_t* s_read = o_done + 2;                                   // [2]
     uint64_t* q_full = s_read + 2;
     uint64_t* q_free = q_full + 1;
-    uint64_t* drain = q_free + 1;                                    // [2]
+    uint64_t* q_staged = q_free + 1;
+    uint64_t* turn = q_staged + 1;                                   // [2][4] per group and lane quarter
+    uint64_t* drain = turn + 8;                                      // [2]
     uint32_t* tmem_slot = (uint32_t*)(drain + 2);
     __shared__ int abort_s;
     __shared__ long long sums[kThreads / 32];
@@ -74,7 +87,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int4* rec = (int4*)((uint8_t*)p.counters + kJoinRecords) + 2 * blockIdx.x;
     if (tid == 0) {
-        for (int i = 0; i < S; ++i) {
+        for (int i = 0; i < 2 * S; ++i) {
             mbar_init(&kv_full[i], 1);
             mbar_init(&kv_empty[i], 1);
         }
@@ -87,21 +100,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
         }
         mbar_init(q_full, 4);
         mbar_init(q_free, 8);
+        mbar_init(q_staged, 32);
+        for (int i = 0; i < 8; ++i) mbar_init(&turn[i], 1);
         abort_s = 0;
         fence_mbar_init();
         tma_prefetch_desc(&p.tmap_half);
     }
     griddep_wait();
     Line line;
-    const long long U = line_plan<kThreads, D>(p, line, line_mem, sums, kOverhead);
-    const int P = (int)min((long long)gridDim.x, max(1ll, U / kMinShare));
+    const int U = line_plan<kThreads, D>(p, line, line_mem, sums, kOverhead);
+    const int P = min((int)gridDim.x, max(1, U / kMinShare));
     if (tid == 64) rec[0] = make_int4(-1, 0, 0, 0);      // no item to join from here, so far
     if (U == 0 || (int)blockIdx.x >= P) return;
     Walker walk;
-    walk.start(line, blockIdx.x * U / P, (blockIdx.x + 1) * U / P);
+    walk.start(line, line_begin(blockIdx.x, U, P), line_begin(blockIdx.x + 1, U, P));
     Stretch s;
     uint32_t tmem = 0;
-    if (warp > 0) {      // the producer does not wait for the tensor memory
+    if (warp > 0 && warp <= kPvWarp) {      // the producers do not wait for the tensor memory
         if (warp == 1) {
             tmem_alloc(tmem_slot, C::COLS);
             // The next kernel may start only once this CTA holds its tensor memory: a dependent
@@ -109,48 +124,69 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             griddep_launch();
         }
         tc_fence_before();
-        named_bar_sync(2, kThreads - 32);
+        named_bar_sync(2, kThreads - 64);
         tc_fence_after();
         tmem = *tmem_slot;
     }
     const uint32_t tS = tmem + C::T_S, tP = tmem + C::T_P, tQ = tmem + C::T_Q, tO = tmem + C::T_O;
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ TMA producer
+    if (warp == 0 || warp > kPvWarp) {
+        // ------------------------------------------------------------ TMA producers, K and V
+        // Rings of their own: a K tile is free again as soon as its S is done, a V tile when its
+        // product is (one ring for both held every stage for the softmax's time too: 4 stages
+        // then cost 1090 cycles a tile, whatever the softmax did).
+        const int kind = warp == 0 ? 0 : 1;
+        uint64_t *full = kv_full + kind * S, *empty = kv_empty + kind * S;
+        uint8_t* tiles = ring + kind * S * C::KV;
         const int bl = p.table ? min(p.ps_log2, 6) : 6;          // log2 rows of a box
         const int box_rows = 1 << bl, boxes = 64 >> bl;
-        int it = 0;
+        const int b = lane & (boxes - 1), h = lane / boxes;       // this lane's box and 64-column half
+        int it = 0, seg = 0;
         bool ok = true;
-        while (ok && walk.next(line, s)) {
+        for (; ok && walk.next(line, s); ++seg) {
             const int4 e = line.ent[s.i];
             const int hi = p.causal ? e.w + s.r1 : e.w + e.z;
             const int lo = p.window > 0 ? max(0, e.w + s.r0 - p.window + 1) : 0;
+            if (kind == 0) {
+                // the stretch's Q, whole rows per group of lanes (a softmax lane that read its own
+                // 256-byte row from global memory touched 32 lines per load: 2500 cycles; one bulk
+                // copy per row took 7000); the softmax has taken the one before
+                if (seg > 0) ok = mbar_wait_short(q_full, (uint32_t)((seg - 1) & 1), abort_flag, p.wait_status);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const int nvec = (s.r1 - s.r0) * p.G, c = lane % (D / 8) * 8;
+                const __nv_bfloat16* src = (const __nv_bfloat16*)p.q + (size_t)(e.y + s.r0) * p.q_stride + s.g * p.G * D + c;
+                const uint32_t dst = smem_u32(q_stage) + c * 2;
+#pragma unroll 4
+                for (int v = lane / (D / 8); v < nvec; v += 256 / D) {
+                    const int r = v * p.g_magic >> 16, x = v - r * p.G;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                                 ::"r"(dst + v * C::QLD), "l"((uint64_t)(src + r * p.q_stride + x * D)) : "memory");
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(q_staged)) : "memory");
+            }
             PageLookup look;
             look.reset();
             for (int t = s.t0; t < s.t1; ++t, ++it) {
-                const int k0 = s.span.tile(t) * 64, st = it % S;
-                // lane (kind, half, box)
-                const int b = lane & (boxes - 1), h = lane / boxes % C::HALVES, kind = lane / boxes / C::HALVES;
-                const int kb = k0 + b * box_rows;
+                const int k0 = s.span.tile(t) * 64, st = it % S, kb = k0 + b * box_rows;
                 const int page = look.at(p, e.x, k0, kb, boxes, lane);
-                const bool want = kind < 2 && kb < hi && (kb < p.sinks || kb + box_rows > lo) && page >= 0;
-                ok = mbar_wait(&kv_empty[st], (uint32_t)(((it / S) & 1) ^ 1), abort_flag, p.wait_status);
+                const bool want = h < C::HALVES && kb < hi && (kb < p.sinks || kb + box_rows > lo) && page >= 0;
+                ok = mbar_wait_short(&empty[st], (uint32_t)(((it / S) & 1) ^ 1), abort_flag, p.wait_status);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
                 }
                 const int n_want = __popc(__ballot_sync(0xffffffffu, want));
-                if (lane == 0) mbar_arrive_expect_tx(&kv_full[st], (uint32_t)(n_want * box_rows * 128));
+                if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(n_want * box_rows * 128));
                 __syncwarp();
                 if (want) {
                     const long long row = (long long)page * p.rows_page + p.row_layer + (long long)s.g * p.rows_kv +
                                           kind * p.rows_kind + (p.table ? kb & ((1 << p.ps_log2) - 1) : kb);
-                    uint8_t* dst = ring + (st * 2 + kind) * C::KV + h * 8192 + b * box_rows * 128;
                     asm volatile(
                         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
                         "[%0], [%1, {%2, %3, %4}], [%5];"
-                        ::"r"(smem_u32(dst)), "l"((uint64_t)&p.tmap_half), "r"(0), "r"((int)row), "r"(h),
-                          "r"(smem_u32(&kv_full[st]))
+                        ::"r"(smem_u32(tiles + st * C::KV + h * 8192 + b * box_rows * 128)), "l"((uint64_t)&p.tmap_half),
+                          "r"(0), "r"((int)row), "r"(h), "r"(smem_u32(&full[st]))
                         : "memory");
                 }
             }
@@ -158,7 +194,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
         if (!ok) {
             // an abandoned launch: its copies land before the CTA exits
             volatile int never = 0;
-            for (int k = max(0, it - S); k < it; ++k) mbar_wait(&kv_full[k % S], (uint32_t)((k / S) & 1), &never, nullptr);
+            for (int k = max(0, it - S); k < it; ++k) mbar_wait_short(&full[k % S], (uint32_t)((k / S) & 1), &never, nullptr);
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ S = Q K^T
@@ -171,21 +208,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
         int it = 0, seg = 0;
         bool ok = true;
         for (; ok && walk.next(line, s); ++seg) {
-            ok = __all_sync(0xffffffffu, mbar_wait(q_full, (uint32_t)(seg & 1), abort_flag, p.wait_status));
+            ok = __all_sync(0xffffffffu, mbar_wait_short(q_full, (uint32_t)(seg & 1), abort_flag, p.wait_status));
             for (int t = s.t0; t < s.t1 && ok; ++t, ++it) {
                 const int st = it % S;
-                ok = mbar_wait(&kv_full[st], (uint32_t)((it / S) & 1), abort_flag, p.wait_status);
-                if (ok && it >= 2) ok = mbar_wait(&s_read[it & 1], (uint32_t)(((it - 2) >> 1) & 1), abort_flag, p.wait_status);
+                ok = mbar_wait_short(&kv_full[st], (uint32_t)((it / S) & 1), abort_flag, p.wait_status);
+                if (ok && it >= 2) ok = mbar_wait_short(&s_read[it & 1], (uint32_t)(((it - 2) >> 1) & 1), abort_flag, p.wait_status);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t ka = smem_u32(ring + st * 2 * C::KV), d = tS + (it & 1) * 64;
+                const uint32_t ka = smem_u32(ring + st * C::KV), d = tS + (it & 1) * 64;
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
                         tc_mma_bf16_ts(d, tQ + kk * 8, umma_desc_sw128(ka + (kk >> 2) * 8192) + 2 * (kk & 3), IDESC_S,
                                        kk > 0 ? 1u : 0u);
                     tc_commit(&s_full[it & 1]);
+                    tc_commit(&kv_empty[st]);
                 }
                 __syncwarp();
             }
@@ -194,9 +232,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             if (leader) tc_commit(&drain[0]);   // the issued MMAs finish before the tensor memory is released
             __syncwarp();
             volatile int never = 0;
-            mbar_wait(&drain[0], 0, &never, nullptr);
+            mbar_wait_short(&drain[0], 0, &never, nullptr);
         }
-    } else if (warp == 10) {
+    } else if (warp == kPvWarp) {
         // ------------------------------------------------------------ O += P V
         constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, true);
         const bool leader = elect_one();
@@ -205,11 +243,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
         while (ok && walk.next(line, s)) {
             for (int t = s.t0; t < s.t1; ++t, ++it) {
                 const int pb = it & 1;
-                ok = mbar_wait(&p_full[pb], (uint32_t)((it >> 1) & 1), abort_flag, p.wait_status);
+                ok = mbar_wait_short(&kv_full[S + it % S], (uint32_t)((it / S) & 1), abort_flag, p.wait_status);
+                if (ok) ok = mbar_wait_short(&p_full[pb], (uint32_t)((it >> 1) & 1), abort_flag, p.wait_status);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t va = smem_u32(ring + ((it % S) * 2 + 1) * C::KV), d = tO + pb * 128, a = tP + pb * 32;
+                const uint32_t va = smem_u32(ring + (S + it % S) * C::KV), d = tO + pb * 128, a = tP + pb * 32;
                 const uint32_t add = t >= s.t0 + 2 ? 1u : 0u;
                 if (leader) {
 #pragma unroll
@@ -217,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                         tc_mma_bf16_ts(d, a + kk * 8, umma_desc_sw128_mn(va + kk * 2048, 8192, 1024), IDESC_PV,
                                        kk > 0 ? 1u : add);
                     tc_commit(&o_done[pb]);
-                    tc_commit(&kv_empty[it % S]);      // S of this tile was done before its P
+                    tc_commit(&kv_empty[S + it % S]);
                 }
                 __syncwarp();
             }
@@ -226,35 +265,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             if (leader) tc_commit(&drain[1]);
             __syncwarp();
             volatile int never = 0;
-            mbar_wait(&drain[1], 0, &never, nullptr);
+            mbar_wait_short(&drain[1], 0, &never, nullptr);
         }
     } else {
         // ------------------------------------------------------------ softmax
         const int w = (warp - 2) >> 2, q4 = warp & 3, rl = q4 * 32 + lane;
-        const int row = rl % RW, cs = rl / RW;                 // vector of the tile, key slice (warp-uniform)
+        const int row = rl % RW, cs = rl / RW, col = cs * KC;  // vector of the tile, first column (warp-uniform)
         const int e256 = tid - 64;
         const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
         const uint32_t my_s = tS + lanes + w * 64, my_p = tP + lanes + w * 32, my_o = tO + lanes + w * 128;
-        // the lane's vector of stretch x into the Q operand (zero past the tile's vectors)
-        auto put_q = [&](const Stretch& x) {
-            const int4 e = line.ent[x.i];
-            const bool have = row < (x.r1 - x.r0) * p.G;
-            const __nv_bfloat16* src = (const __nv_bfloat16*)p.q + (size_t)(e.y + x.r0 + row / p.G) * p.q_stride +
-                                       (size_t)(x.g * p.G + row % p.G) * D;
-            uint4 qv[D / 8];
-#pragma unroll
-            for (int k = 0; k < D / 8; ++k)
-                qv[k] = have ? *reinterpret_cast<const uint4*>(src + 8 * k) : make_uint4(0, 0, 0, 0);
-#pragma unroll
+        // the lane's vector of stretch n (staged by the producer) into the Q operand; lanes past the
+        // tile's vectors take whatever stands there (their rows are not written)
+        auto put_q = [&](int n) -> bool {
+            bool got = mbar_wait_short(q_staged, (uint32_t)(n & 1), abort_flag, p.wait_status);
+            if (!__all_sync(0xffffffffu, got)) return false;
+            const uint8_t* src = q_stage + row * C::QLD;
+#pragma unroll 1
             for (int c0 = 0; c0 < D / 2; c0 += 16) {
                 float v[16];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const uint4 u = qv[c0 / 4 + k];
-                    v[4 * k + 0] = __uint_as_float(u.x);
-                    v[4 * k + 1] = __uint_as_float(u.y);
-                    v[4 * k + 2] = __uint_as_float(u.z);
-                    v[4 * k + 3] = __uint_as_float(u.w);
+                    const float4 u = *reinterpret_cast<const float4*>(src + (c0 + 4 * k) * 4);
+                    v[4 * k + 0] = u.x;
+                    v[4 * k + 1] = u.y;
+                    v[4 * k + 2] = u.z;
+                    v[4 * k + 3] = u.w;
                 }
                 tmem_st16(tQ + lanes + c0, v);
             }
@@ -262,6 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
+            return true;
         };
         Stretch nx;
         bool more = walk.next(line, nx);
@@ -271,15 +307,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             for (int c0 = 0; c0 < 32; c0 += 8) tmem_st8u(my_p + c0, z);
             tmem_wait_st();
         }
-        if (more && w == 0) put_q(nx);
         int it0 = 0, seg = 0;             // tiles and stretches before this one
         bool ok = true;
-        while (more && ok) {
+        if (more && w == 0) ok = put_q(0);
+        while (more) {               // left by all threads together
             s = nx;
-            more = walk.next(line, nx);
             const int4 e = line.ent[s.i];
             const int nvec = (s.r1 - s.r0) * p.G;
-            const int pos = e.w + s.r0 + row / p.G;                    // this lane's position (padding lanes: any)
+            const int pos = e.w + s.r0 + (row * p.g_magic >> 16);                    // this lane's position (padding lanes: any)
             const int hi_tile = p.causal ? e.w + s.r1 : e.w + e.z;     // keys that exist for some row
             const int lo_tile = p.window > 0 ? max(0, e.w + s.r0 - p.window + 1) : 0;
             const int hi_all = p.causal ? e.w + s.r0 + 1 : hi_tile;    // keys below are seen by all rows ..
@@ -288,44 +323,48 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             const int lo_row = p.window > 0 ? pos - p.window + 1 : 0;
             float base = -INFINITY, l = 0.f;
             int last = -1;                                             // this group's last tile
-            for (int t = s.t0 + ((it0 ^ w) & 1); t < s.t1; t += 2) {
+            for (int t = s.t0 + ((it0 ^ w) & 1); ok && t < s.t1; t += 2) {
                 const int it = it0 + t - s.t0;
                 last = it;
-                ok = mbar_wait(&s_full[w], (uint32_t)((it >> 1) & 1), abort_flag, p.wait_status);
+                ok = mbar_wait_short(&s_full[w], (uint32_t)((it >> 1) & 1), abort_flag, p.wait_status);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
                 // the product of the group's tile before has read P and written O (looked at early,
                 // waited for where it matters)
                 const bool o_ready = it < 2 || mbar_test(&o_done[w], (uint32_t)(((it - 2) >> 1) & 1));
-                const int k0 = s.span.tile(t) * 64, kvb = k0 + cs * KC;
+                const int k0 = s.span.tile(t) * 64, kvb = k0 + col;
                 float x[KC];
-                if constexpr (KC == 64) {
-                    tmem_ld32w(my_s, x);
-                    tmem_ld32w(my_s + 32, x + 32);
-                } else if constexpr (KC == 32) {
-                    tmem_ld32w(my_s + cs * KC, x);
-                } else {
-                    tmem_ld16w(my_s + cs * KC, x);
-                }
+                if constexpr (KC == 64) tmem_ld64w(my_s, x);
+                else if constexpr (KC == 32) tmem_ld32w(my_s + col, x);
+                else tmem_ld16w(my_s + col, x);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s_read[w]);
                 // tiles with keys that some row does not see
                 if (k0 + 64 > hi_all || (k0 < lo_all && k0 + 64 > p.sinks)) {
+                    // this thread's keys as bits: below the row's end, and from its window on or a sink
 #pragma unroll
-                    for (int i = 0; i < KC; ++i) {
-                        const int k = kvb + i;
-                        if (!(k < hi_row && (k >= lo_row || k < p.sinks))) x[i] = -INFINITY;
+                    for (int c0 = 0; c0 < KC; c0 += 32) {
+                        const int k = kvb + c0;
+                        const uint32_t m = bits_below(hi_row - k) & (~bits_below(lo_row - k) | bits_below(p.sinks - k));
+#pragma unroll
+                        for (int i = 0; i < (KC < 32 ? KC : 32); ++i)
+                            if (!(m & (1u << i))) x[c0 + i] = -INFINITY;
                     }
                     // V rows that no row sees may hold anything (0 * NaN is NaN): zero them
-                    uint8_t* vs = ring + ((it % S) * 2 + 1) * C::KV;
-                    for (int idx = rl; idx < 64 * C::HALVES * 8; idx += 128) {
-                        const int r = idx / (C::HALVES * 8), rem = idx % (C::HALVES * 8), k = k0 + r;
-                        if (k >= hi_tile || (k < lo_tile && k >= p.sinks))
-                            *reinterpret_cast<uint4*>(vs + (rem / 8) * 8192 + r * 128 + (rem % 8) * 16) = make_uint4(0, 0, 0, 0);
+                    if (k0 + 64 > hi_tile || (k0 < lo_tile && k0 + 64 > p.sinks)) {
+                        mbar_wait_short(&kv_full[S + it % S], (uint32_t)((it / S) & 1), abort_flag, p.wait_status);
+                        // two threads to a row
+                        const int k = k0 + (rl >> 1);
+                        if (k >= hi_tile || (k < lo_tile && k >= p.sinks)) {
+                            uint8_t* vr = ring + (S + it % S) * C::KV + (rl >> 1) * 128 + (rl & 1) * 64;
+#pragma unroll
+                            for (int x4 = 0; x4 < C::HALVES * 4; ++x4)
+                                *reinterpret_cast<uint4*>(vr + (x4 >> 2) * 8192 + (x4 & 3) * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async();   // the product reads these rows through the async proxy
                     }
-                    fence_proxy_async();   // the product reads these rows through the async proxy
                 }
                 float m8[8];
 #pragma unroll
@@ -336,27 +375,38 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                                               fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * p.scale_log2);
                 const bool grow = nb > base + kBaseLag;
                 if (!__all_sync(0xffffffffu, o_ready)) {
-                    ok = mbar_wait(&o_done[w], (uint32_t)(((it - 2) >> 1) & 1), abort_flag, p.wait_status);
+                    ok = mbar_wait_short(&o_done[w], (uint32_t)(((it - 2) >> 1) & 1), abort_flag, p.wait_status);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                 }
                 tc_fence_after();
                 if (__any_sync(0xffffffffu, grow)) {
                     if (t >= s.t0 + 2) {   // O holds earlier tiles
-                        const float f = grow ? exp2f(base - nb) : 1.0f;
+                        const float f = grow ? exp2f(base - nb - kBaseLead) : 1.0f;
 #pragma unroll 1
-                        for (int c0 = 0; c0 < D; c0 += 16) {
-                            float v[16];
-                            tmem_ld16w(my_o + c0, v);
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            float v[32];
+                            tmem_ld32w(my_o + c0, v);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) v[i] *= f;
+                            for (int i = 0; i < 32; ++i) v[i] *= f;
                             tmem_st16(my_o + c0, v);
+                            tmem_st16(my_o + c0 + 16, v + 16);
                         }
                         l *= f;
                     }
-                    if (grow) base = nb;
+                    if (grow) base = nb + kBaseLead;
                 }
                 const float bb = (base == -INFINITY) ? 0.f : base;
+                if constexpr (CS == 1) {
+                    // the two warps of a quarter share an SM partition: they exponentiate in turn (in
+                    // step with one another both took 2200 cycles a tile, in turn 1400)
+                    if (it >= 1) {
+                        ok = mbar_wait_short(&turn[w * 4 + q4], (uint32_t)(((it >> 1) - (w == 0 ? 1 : 0)) & 1), abort_flag,
+                                             p.wait_status);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                    }
+                }
                 float ls[KC / 16];
 #pragma unroll
                 for (int c0 = 0; c0 < KC; c0 += 16) {
@@ -370,7 +420,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                         pk[i / 2] = pack_bf16(e0, e1);
                     }
                     ls[c0 >> 4] = s2;
-                    tmem_st8u(my_p + cs * (KC / 2) + c0 / 2, pk);
+                    tmem_st8u(my_p + col / 2 + c0 / 2, pk);
+                }
+                if constexpr (CS == 1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&turn[(w ^ 1) * 4 + q4]);
                 }
 #pragma unroll
                 for (int i = 0; i < KC / 16; ++i) l += ls[i];
@@ -382,19 +436,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             // this warp has read its last S of the stretch; when all have, Q may change
             __syncwarp();
             if (lane == 0) mbar_arrive(q_free);
+            more = walk.next(line, nx);
             if (ok && more && w == 0) {
-                ok = mbar_wait(q_free, (uint32_t)(seg & 1), abort_flag, p.wait_status);
+                ok = mbar_wait_short(q_free, (uint32_t)(seg & 1), abort_flag, p.wait_status);
                 ok = __all_sync(0xffffffffu, ok);
-                if (ok) put_q(nx);
+                if (ok) ok = put_q(seg + 1);
             }
             ++seg;
             if (ok && last >= 0)
-                ok = mbar_wait(&o_done[w], (uint32_t)((last >> 1) & 1), abort_flag, p.wait_status);
+                ok = mbar_wait_short(&o_done[w], (uint32_t)((last >> 1) & 1), abort_flag, p.wait_status);
             ml[w * 128 + rl] = make_float2(base, l);
-            if (named_bar_or(1, kSoftmax, !ok)) {
-                ok = false;
-                break;
-            }
+            if (named_bar_or(1, kSoftmax, !ok)) break;
             tc_fence_after();
             // ---- the stretch's rows: the groups' O are added, then the copies of a vector.  Bases
             // differ by integers, so all factors are exact powers of two.
@@ -402,17 +454,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             float* slot = p.partial + (size_t)(2 * blockIdx.x + (head ? 1 : 0)) * C::SLOT;
             if constexpr (CS == 1) {
                 // each group finishes half the columns: it gives the other half away
-                const float2 other = ml[(w ^ 1) * 128 + rl];
-                const float B = fmaxf(base, other.x), z = B == -INFINITY ? 0.f : B;
-                const float f0 = last >= 0 ? exp2f(base - z) : 0.f, f1 = exp2f(other.x - z);
-                const float L = f0 * l + f1 * other.y, inv = L == 0.f ? 0.f : 1.0f / L;
+                constexpr int HC = D / 2;
+                const float2 m0 = ml[rl], m1 = ml[128 + rl];
+                const float B = fmaxf(m0.x, m1.x), z = B == -INFINITY ? 0.f : B;
+                const float g0 = exp2f(m0.x - z), g1 = exp2f(m1.x - z), f0 = w ? g1 : g0;
+                const float L = g0 * m0.y + g1 * m1.y, inv = L == 0.f ? 0.f : 1.0f / L;
                 float* mine = join + (w * 128 + rl) * C::HLD;
-                const float* theirs = join + ((w ^ 1) * 128 + rl) * C::HLD;
-                const uint32_t keep = my_o + w * (D / 2), give = my_o + (w ^ 1) * (D / 2);
-#pragma unroll
-                for (int c0 = 0; c0 < D / 2; c0 += 32) {
+                float* theirs = join + ((w ^ 1) * 128 + rl) * C::HLD;
+#pragma unroll 1
+                for (int c0 = 0; c0 < HC; c0 += 32) {
                     float v[32];
-                    tmem_ld32w(give + c0, v);
+                    tmem_ld32w(my_o + (w ^ 1) * HC + c0, v);
 #pragma unroll
                     for (int i = 0; i < 32; i += 4)
                         *reinterpret_cast<float4*>(mine + c0 + i) =
@@ -420,13 +472,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                                       : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
                 named_bar_sync(1, kSoftmax);
-                __nv_bfloat16* dst = (__nv_bfloat16*)p.out +
-                                     ((size_t)(e.y + s.r0 + row / p.G) * p.nq + (size_t)s.g * p.G + row % p.G) * D + w * (D / 2);
-                float* part = slot + 256 + row * D + w * (D / 2);
-#pragma unroll
-                for (int c0 = 0; c0 < D / 2; c0 += 32) {
+#pragma unroll 1
+                for (int c0 = 0; c0 < HC; c0 += 32) {
                     float v[32];
-                    tmem_ld32w(keep + c0, v);
+                    tmem_ld32w(my_o + w * HC + c0, v);
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
                         const float4 o = *reinterpret_cast<const float4*>(theirs + c0 + i);
@@ -435,21 +484,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                         v[i + 2] = (last >= 0 ? f0 * v[i + 2] : 0.f) + o.z;
                         v[i + 3] = (last >= 0 ? f0 * v[i + 3] : 0.f) + o.w;
                     }
-                    if (row < nvec) {
-                        if (whole) {
+                    if (whole) {      // as bf16 over what was just read; written out below
 #pragma unroll
-                            for (int i = 0; i < 32; i += 8)
-                                *reinterpret_cast<uint4*>(dst + c0 + i) =
-                                    make_uint4(pack_bf16(v[i] * inv, v[i + 1] * inv), pack_bf16(v[i + 2] * inv, v[i + 3] * inv),
-                                               pack_bf16(v[i + 4] * inv, v[i + 5] * inv), pack_bf16(v[i + 6] * inv, v[i + 7] * inv));
-                        } else {
+                        for (int i = 0; i < 32; i += 8)
+                            *reinterpret_cast<uint4*>((uint8_t*)(theirs + c0) + i * 2) =
+                                make_uint4(pack_bf16(v[i] * inv, v[i + 1] * inv), pack_bf16(v[i + 2] * inv, v[i + 3] * inv),
+                                           pack_bf16(v[i + 4] * inv, v[i + 5] * inv), pack_bf16(v[i + 6] * inv, v[i + 7] * inv));
+                    } else if (row < nvec) {
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4)
-                                *reinterpret_cast<float4*>(part + c0 + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                        }
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<float4*>(slot + part_at(row, w * HC + c0 + i)) =
+                                make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                     }
                 }
-                if (!whole && w == 0 && row < nvec) *reinterpret_cast<float2*>(slot + 2 * row) = make_float2(B, L);
+                if (whole) {
+                    named_bar_sync(1, kSoftmax);
+                    // whole 256-byte (128-byte) rows per group of lanes
+                    __nv_bfloat16* out0 = (__nv_bfloat16*)p.out + ((size_t)(e.y + s.r0) * p.nq + (size_t)s.g * p.G) * D;
+#pragma unroll 4
+                    for (int i = e256; i < nvec * (D / 8); i += kSoftmax) {
+                        const int v = i / (D / 8), c = (i % (D / 8)) * 8;
+                        const uint4 u = *reinterpret_cast<const uint4*>(
+                            (const uint8_t*)(join + ((c / HC ^ 1) * 128 + v) * C::HLD + (c % HC & ~31)) + (c & 31) * 2);
+                        const int vr = v * p.g_magic >> 16;
+                        *reinterpret_cast<uint4*>(out0 + ((size_t)vr * p.nq + (v - vr * p.G)) * D + c) = u;
+                    }
+                } else if (w == 0 && row < nvec) {
+                    *reinterpret_cast<float2*>(slot + 2 * row) = make_float2(B, L);
+                }
             } else {
                 // group 1's O to shared memory, group 0 adds its own
                 if (w == 1) {
@@ -486,35 +548,38 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                     ml[rl] = make_float2(B, f0 * l + f1 * other.y);
                 }
                 named_bar_sync(1, kSoftmax);
-            for (int i = e256; i < nvec * (D / 8); i += kSoftmax) {
-                const int v = i / (D / 8), c = (i % (D / 8)) * 8;
-                float B = -INFINITY, L = 0.f, a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                // rows in order for the output, columns in order for a partial
+#pragma unroll 1
+                for (int i = e256; i < RW * (D / 8); i += kSoftmax) {
+                    const int v = whole ? i / (D / 8) : i % RW, c = (whole ? i % (D / 8) : i / RW) * 8;
+                    if (v >= nvec) continue;
+                    float B = -INFINITY, L = 0.f, a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int k = 0; k < CS; ++k) B = fmaxf(B, ml[v + k * RW].x);
-                const float z = B == -INFINITY ? 0.f : B;
+                    for (int k = 0; k < CS; ++k) B = fmaxf(B, ml[v + k * RW].x);
+                    const float z = B == -INFINITY ? 0.f : B;
 #pragma unroll
-                for (int k = 0; k < CS; ++k) {
-                    const float2 m = ml[v + k * RW];
-                    const float f = exp2f(m.x - z);
-                    const float4 w0 = *reinterpret_cast<const float4*>(join + (v + k * RW) * C::OLD + c);
-                    const float4 w1 = *reinterpret_cast<const float4*>(join + (v + k * RW) * C::OLD + c + 4);
-                    L += f * m.y;
-                    a[0] += f * w0.x; a[1] += f * w0.y; a[2] += f * w0.z; a[3] += f * w0.w;
-                    a[4] += f * w1.x; a[5] += f * w1.y; a[6] += f * w1.z; a[7] += f * w1.w;
+                    for (int k = 0; k < CS; ++k) {
+                        const float2 m = ml[v + k * RW];
+                        const float f = exp2f(m.x - z);
+                        const float4 w0 = *reinterpret_cast<const float4*>(join + (v + k * RW) * C::OLD + c);
+                        const float4 w1 = *reinterpret_cast<const float4*>(join + (v + k * RW) * C::OLD + c + 4);
+                        L += f * m.y;
+                        a[0] += f * w0.x; a[1] += f * w0.y; a[2] += f * w0.z; a[3] += f * w0.w;
+                        a[4] += f * w1.x; a[5] += f * w1.y; a[6] += f * w1.z; a[7] += f * w1.w;
+                    }
+                    if (whole) {
+                        const float inv = L == 0.f ? 0.f : 1.0f / L;
+                        __nv_bfloat16* dst = (__nv_bfloat16*)p.out +
+                                             ((size_t)(e.y + s.r0 + v / p.G) * p.nq + (size_t)s.g * p.G + v % p.G) * D + c;
+                        *reinterpret_cast<uint4*>(dst) =
+                            make_uint4(pack_bf16(a[0] * inv, a[1] * inv), pack_bf16(a[2] * inv, a[3] * inv),
+                                       pack_bf16(a[4] * inv, a[5] * inv), pack_bf16(a[6] * inv, a[7] * inv));
+                    } else {
+                        *reinterpret_cast<float4*>(slot + part_at(v, c)) = make_float4(a[0], a[1], a[2], a[3]);
+                        *reinterpret_cast<float4*>(slot + part_at(v, c + 4)) = make_float4(a[4], a[5], a[6], a[7]);
+                        if (c == 0) *reinterpret_cast<float2*>(slot + 2 * v) = make_float2(B, L);
+                    }
                 }
-                if (whole) {
-                    const float inv = L == 0.f ? 0.f : 1.0f / L;
-                    __nv_bfloat16* dst = (__nv_bfloat16*)p.out +
-                                         ((size_t)(e.y + s.r0 + v / p.G) * p.nq + (size_t)s.g * p.G + v % p.G) * D + c;
-                    *reinterpret_cast<uint4*>(dst) =
-                        make_uint4(pack_bf16(a[0] * inv, a[1] * inv), pack_bf16(a[2] * inv, a[3] * inv),
-                                   pack_bf16(a[4] * inv, a[5] * inv), pack_bf16(a[6] * inv, a[7] * inv));
-                } else {
-                    *reinterpret_cast<float4*>(slot + 256 + v * D + c) = make_float4(a[0], a[1], a[2], a[3]);
-                    *reinterpret_cast<float4*>(slot + 256 + v * D + c + 4) = make_float4(a[4], a[5], a[6], a[7]);
-                    if (c == 0) *reinterpret_cast<float2*>(slot + 2 * v) = make_float2(B, L);
-                }
-            }
             }
             if (!whole && head && e256 == 0) {
                 rec[0] = make_int4(line_owner(s.v0 + kOverhead + s.span.nt - 1, U, P), nvec, e.y + s.r0, s.g);
@@ -542,7 +607,7 @@ __global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ Page
     const int4 rec = *((const int4*)((const uint8_t*)p.counters + kJoinRecords) + 2 * c0);
     const int i = blockIdx.y * 256 + threadIdx.x;
     if (rec.x < 0 || i >= rec.y * (D / 8)) return;
-    const int v = i / (D / 8), c = (i % (D / 8)) * 8;
+    const int v = i % rec.y, c = i / rec.y * 8;
     float B = -INFINITY, L = 0.f, a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int k0 = c0; k0 <= rec.x; k0 += 4) {     // four partials' loads in flight
         float2 m[4];
@@ -552,8 +617,8 @@ __global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ Page
             const int cta = min(k0 + k, rec.x);
             const float* q = p.partial + (size_t)(2 * cta + (cta == c0 ? 1 : 0)) * SLOT;
             m[k] = *reinterpret_cast<const float2*>(q + 2 * v);
-            w0[k] = *reinterpret_cast<const float4*>(q + 256 + v * D + c);
-            w1[k] = *reinterpret_cast<const float4*>(q + 256 + v * D + c + 4);
+            w0[k] = *reinterpret_cast<const float4*>(q + part_at(v, c));
+            w1[k] = *reinterpret_cast<const float4*>(q + part_at(v, c + 4));
         }
         float nb = B;
 #pragma unroll
@@ -599,6 +664,7 @@ int launch_d(const PagedAttnParams& p, int vectors, int num_sms, cudaStream_t st
 }  // namespace
 
 int launch_paged_block(PagedAttnParams& p, int d, int num_sms, cudaStream_t st) {
+    p.g_magic = (65536 + p.G - 1) / p.G;
     p.launches = 2;
     p.rt = std::min(p.max_rows, kPagedRowsTc / p.G);
     p.row_tiles = (p.max_rows + p.rt - 1) / p.rt;

@@ -3,8 +3,8 @@
 // joined.
 //
 // With t_k = q.k log2(e) / sqrt(d), out = sum_k P_k v_k / sum_k 2^(t_k - b), P_k =
-// bf16(2^(t_k - b)) for an integer b per row.  b follows the running maximum and may
-// lag it by 8: moving b scales everything by an exact power of two, so the split points
+// bf16(2^(t_k - b)) for an integer b per row.  b follows the running maximum (kBaseLag,
+// kBaseLead): moving b scales everything by an exact power of two, so the split points
 // and the order of the keys change no rounding of P.
 //
 // Bound by HBM: every K and V byte is read once, and there are only 2 * rows flops for
@@ -34,7 +34,6 @@ constexpr int kConsumers = 4;
 constexpr int kTileKeys = kLineTile;
 constexpr int kOverhead = 2;   // units that starting and joining an item costs, in tiles
 constexpr int kMinShare = 4;   // smallest share of a CTA, in units
-constexpr float kBaseLag = 8.0f;
 
 template <int D> struct DecodeCfg {
     static constexpr int TILE = kTileKeys * D * 2;           // bytes of a K (or V) tile
@@ -96,11 +95,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
     griddep_launch();
 
     Line line;
-    const long long U = line_plan<kThreads, D>(p, line, line_mem, sums, kOverhead);
-    const int P = (int)min((long long)gridDim.x, max(1ll, U / kMinShare));
+    const int U = line_plan<kThreads, D>(p, line, line_mem, sums, kOverhead);
+    const int P = min((int)gridDim.x, max(1, U / kMinShare));
     if (U == 0 || (int)blockIdx.x >= P) return;
     Walker walk;
-    walk.start(line, blockIdx.x * U / P, (blockIdx.x + 1) * U / P);
+    walk.start(line, line_begin(blockIdx.x, U, P), line_begin(blockIdx.x + 1, U, P));
     Stretch s;
     const int bl = p.table ? min(p.ps_log2, 6) : 6;          // log2 rows of a TMA box
     const int box_rows = 1 << bl, boxes = kTileKeys >> bl;
@@ -121,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
                 const int b = lane & (boxes - 1), kind = lane / boxes, kb = k0 + b * box_rows;
                 const bool want = kind < 2 && kb < hi && (kb < p.sinks || kb + box_rows > lo);
                 const int page = look.at(p, e.x, k0, kb, boxes, lane);
-                ok = mbar_wait(&empty[st], (uint32_t)(((it / S) & 1) ^ 1), abort_flag, p.wait_status);
+                ok = mbar_wait_short(&empty[st], (uint32_t)(((it / S) & 1) ^ 1), abort_flag, p.wait_status);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
@@ -140,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
         if (!ok) {
             // an abandoned launch: its copies land before the CTA exits
             volatile int never = 0;
-            for (int k = max(0, it - S); k < it; ++k) mbar_wait(&full[k % S], (uint32_t)((k / S) & 1), &never, nullptr);
+            for (int k = max(0, it - S); k < it; ++k) mbar_wait_short(&full[k % S], (uint32_t)((k / S) & 1), &never, nullptr);
         }
         return;
     }
@@ -188,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
 
         for (int t = s.t0; t < s.t1; ++t, ++it) {
             const int st = it % S;
-            if (ok) ok = mbar_wait(&full[st], (uint32_t)((it / S) & 1), abort_flag, p.wait_status);
+            if (ok) ok = mbar_wait_short(&full[st], (uint32_t)((it / S) & 1), abort_flag, p.wait_status);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) continue;
             const int kw = s.span.tile(t) * kTileKeys + cw * 16;          // this warp's first key
@@ -235,7 +234,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
                 float xb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
                 xa = floorf(fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 2)));
                 xb = floorf(fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 2)));
-                const float na = xa > base_a + kBaseLag ? xa : base_a, nb = xb > base_b + kBaseLag ? xb : base_b;
+                const float na = xa > base_a + kBaseLag ? xa + kBaseLead : base_a;
+                const float nb = xb > base_b + kBaseLag ? xb + kBaseLead : base_b;
                 const float fa = na == base_a ? 1.f : exp2f(base_a - na), fb = nb == base_b ? 1.f : exp2f(base_b - nb);
                 base_a = na;
                 base_b = nb;
@@ -372,6 +372,7 @@ int launch_d(const PagedAttnParams& p, int num_sms, cudaStream_t st) {
 int launch_paged_decode(PagedAttnParams& p, int d, int num_sms, cudaStream_t st) {
     p.rt = p.max_rows;
     p.row_tiles = 1;
+    p.g_magic = (65536 + p.G - 1) / p.G;
     p.launches = 1;
     return d == 128 ? launch_d<128>(p, num_sms, st) : launch_d<64>(p, num_sms, st);
 }
