@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(q_full);
+            mbar_arrive_if(lane == 0, q_full);
             return true;
         };
         Stretch nx;
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                 else tmem_ld16w(my_s + col, x);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s_read[w]);
+                mbar_arrive_if(lane == 0, &s_read[w]);
                 // tiles with keys that some row does not see
                 if (k0 + 64 > hi_all || (k0 < lo_all && k0 + 64 > p.sinks)) {
                     // this thread's keys as bits: below the row's end, and from its window on or a sink
@@ -366,13 +366,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                         fence_proxy_async();   // the product reads these rows through the async proxy
                     }
                 }
-                float m8[8];
+                float m4[4];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) m8[k] = x[k];
+                for (int k = 0; k < 4; ++k) m4[k] = fmax3(x[3 * k], x[3 * k + 1], x[3 * k + 2]);
 #pragma unroll
-                for (int i = 8; i < KC; ++i) m8[i & 7] = fmaxf(m8[i & 7], x[i]);
-                const float nb = floorf(fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                                              fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * p.scale_log2);
+                for (int i = 12; i + 1 < KC; i += 2) m4[(i >> 1) & 3] = fmax3(m4[(i >> 1) & 3], x[i], x[i + 1]);
+                const float nb = floorf(fmax3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * p.scale_log2);
                 const bool grow = nb > base + kBaseLag;
                 if (!__all_sync(0xffffffffu, o_ready)) {
                     ok = mbar_wait_short(&o_done[w], (uint32_t)(((it - 2) >> 1) & 1), abort_flag, p.wait_status);
@@ -407,35 +406,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                         if (!ok) break;
                     }
                 }
-                float ls[KC / 16];
+                // two at a time where the hardware has it: instructions are what this loop runs out of
+                const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nb2 = make_float2(-bb, -bb);
+                float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int c0 = 0; c0 < KC; c0 += 16) {
-                    float s2 = 0.f;
                     uint32_t pk[8];
 #pragma unroll
                     for (int i = 0; i < 16; i += 2) {
-                        const float e0 = ex2_fast(fmaf(x[c0 + i], p.scale_log2, -bb));
-                        const float e1 = ex2_fast(fmaf(x[c0 + i + 1], p.scale_log2, -bb));
-                        s2 += e0 + e1;
-                        pk[i / 2] = pack_bf16(e0, e1);
+                        const float2 t2 = fma_x2(make_float2(x[c0 + i], x[c0 + i + 1]), sc2, nb2);
+                        const float2 e2 = make_float2(ex2_fast(t2.x), ex2_fast(t2.y));
+                        sum2[(i >> 1) & 1] = add_x2(sum2[(i >> 1) & 1], e2);
+                        pk[i / 2] = pack_bf16(e2.x, e2.y);
                     }
-                    ls[c0 >> 4] = s2;
                     tmem_st8u(my_p + col / 2 + c0 / 2, pk);
                 }
                 if constexpr (CS == 1) {
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&turn[(w ^ 1) * 4 + q4]);
+                    mbar_arrive_if(lane == 0, &turn[(w ^ 1) * 4 + q4]);
                 }
-#pragma unroll
-                for (int i = 0; i < KC / 16; ++i) l += ls[i];
+                sum2[0] = add_x2(sum2[0], sum2[1]);
+                l += sum2[0].x + sum2[0].y;
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[w]);
+                mbar_arrive_if(lane == 0, &p_full[w]);
             }
             // this warp has read its last S of the stretch; when all have, Q may change
             __syncwarp();
-            if (lane == 0) mbar_arrive(q_free);
+            mbar_arrive_if(lane == 0, q_free);
             more = walk.next(line, nx);
             if (ok && more && w == 0) {
                 ok = mbar_wait_short(q_free, (uint32_t)(seg & 1), abort_flag, p.wait_status);
