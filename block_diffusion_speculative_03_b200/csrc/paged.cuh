@@ -371,14 +371,22 @@ struct Walker {
     }
 };
 
-// Bounded wait on an mbarrier phase, as mbar_wait, for waits that are short and many: the
-// clock is first read after 64 tries (reading %globaltimer costs some 300 cycles, which every
-// wait that did not succeed at once paid otherwise).
+// Bounded wait on an mbarrier phase, as mbar_wait, for waits that are short and many: a try
+// may suspend the warp for up to 20 us (a warp that spins takes issue slots from the softmax
+// warps beside it), and the clock is first read after 32 of them.
 DF_DEV bool mbar_wait_short(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
     uint64_t t0 = 0;
     for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 63u) == 0) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+            : "memory");
+        if (ok) return true;
+        if ((it & 31u) == 0) {
             if (*abort_flag) return false;
             const uint64_t now = globaltimer_ns();
             if (t0 == 0) t0 = now;
@@ -390,7 +398,6 @@ DF_DEV bool mbar_wait_short(uint64_t* bar, uint32_t parity, volatile int* abort_
         }
     }
 }
-
 // Arrive without a branch.
 DF_DEV void mbar_arrive_if(bool pred, uint64_t* bar) {
     asm volatile(

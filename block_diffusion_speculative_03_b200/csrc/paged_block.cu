@@ -78,8 +78,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
     uint64_t* q_full = s_read + 2;
     uint64_t* q_free = q_full + 1;
     uint64_t* q_staged = q_free + 1;
-    uint64_t* turn = q_staged + 1;                                   // [2][4] per group and lane quarter
-    uint64_t* drain = turn + 8;                                      // [2]
+    uint64_t* drain = q_staged + 1;                                  // [2]
     uint32_t* tmem_slot = (uint32_t*)(drain + 2);
     __shared__ int abort_s;
     __shared__ long long sums[kThreads / 32];
@@ -101,7 +100,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
         mbar_init(q_full, 4);
         mbar_init(q_free, 8);
         mbar_init(q_staged, 32);
-        for (int i = 0; i < 8; ++i) mbar_init(&turn[i], 1);
         abort_s = 0;
         fence_mbar_init();
         tma_prefetch_desc(&p.tmap_half);
@@ -396,16 +394,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                     if (grow) base = nb + kBaseLead;
                 }
                 const float bb = (base == -INFINITY) ? 0.f : base;
-                if constexpr (CS == 1) {
-                    // the two warps of a quarter share an SM partition: they exponentiate in turn (in
-                    // step with one another both took 2200 cycles a tile, in turn 1400)
-                    if (it >= 1) {
-                        ok = mbar_wait_short(&turn[w * 4 + q4], (uint32_t)(((it >> 1) - (w == 0 ? 1 : 0)) & 1), abort_flag,
-                                             p.wait_status);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) break;
-                    }
-                }
                 // two at a time where the hardware has it: instructions are what this loop runs out of
                 const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nb2 = make_float2(-bb, -bb);
                 float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -420,10 +408,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                         pk[i / 2] = pack_bf16(e2.x, e2.y);
                     }
                     tmem_st8u(my_p + col / 2 + c0 / 2, pk);
-                }
-                if constexpr (CS == 1) {
-                    __syncwarp();
-                    mbar_arrive_if(lane == 0, &turn[(w ^ 1) * 4 + q4]);
                 }
                 sum2[0] = add_x2(sum2[0], sum2[1]);
                 l += sum2[0].x + sum2[0].y;
