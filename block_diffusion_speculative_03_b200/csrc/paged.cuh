@@ -123,11 +123,13 @@ struct AttnEntry {
     int bad;                 // its rows are to be zeroed: [start, start + count)
 };
 DF_DEV AttnEntry attn_entry(const PagedAttnParams& p, int i) {
+    // the loads that do not depend on one another together
     AttnEntry e;
-    e.seq = p.seqs ? p.seqs[i] : i;
     e.start = p.row_start ? p.row_start[i] : i * p.uniform;
     e.count = p.row_start ? p.row_count[i] : p.uniform;
-    e.len = 0;
+    e.seq = p.seqs ? p.seqs[i] : i;
+    const bool exists = e.seq >= 0 && e.seq < p.max_seqs;
+    e.len = p.len[exists ? e.seq : 0];
     e.bad = 0;
     if (e.seq == -1 || e.count == 0) {
         e.count = 0;
@@ -138,11 +140,10 @@ DF_DEV AttnEntry attn_entry(const PagedAttnParams& p, int i) {
         e.bad = DFLASH_INVALID_ARG;   // not a row range: nothing can be zeroed
         return e;
     }
-    if (e.seq < 0 || e.seq >= p.max_seqs) {
+    if (!exists) {
         e.bad = DFLASH_INVALID_ARG;
         return e;
     }
-    e.len = p.len[e.seq];
     if (p.table) {
         const long long last = ((long long)e.len + e.count - 1) >> p.ps_log2;
         if (last >= p.max_pages || p.table[(size_t)e.seq * p.max_pages + last] < 0) e.bad = DFLASH_CAPACITY;

@@ -58,6 +58,25 @@ DF_DEV uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu :
 // one another (a warp's lanes hold consecutive vectors: whole lines per store).
 DF_DEV int part_at(int v, int c) { return 256 + ((c >> 2) * 128 + v) * 4 + (c & 3); }
 
+// Vectors [v0, v1) of a stretch's Q to q_stage by thread x of n (a multiple of 32): 16-byte
+// pieces, whole rows per group of lanes.  (A softmax lane that read its own 256-byte row from
+// global memory touched 32 lines per load: 2500 cycles; one bulk copy per row took 7000.)
+template <int D>
+DF_DEV void stage_q(const PagedAttnParams& p, const Line& line, const Stretch& s, uint8_t* q_stage, int v0, int v1, int x,
+                    int n) {
+    const int4 e = line.ent[s.i];
+    const int c = x % (D / 8) * 8, step = n / (D / 8);
+    v1 = min(v1, (s.r1 - s.r0) * p.G);
+#pragma unroll 2
+    for (int v = v0 + x / (D / 8); v < v1; v += step) {
+        const int r = v * p.g_magic >> 16;
+        const __nv_bfloat16* src = (const __nv_bfloat16*)p.q + (size_t)(e.y + s.r0 + r) * p.q_stride +
+                                   (s.g * p.G + v - r * p.G) * D + c;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                     ::"r"(smem_u32(q_stage) + v * BlockCfg<D>::QLD + c * 2), "l"((uint64_t)src) : "memory");
+    }
+}
+
 template <int D, int CS>
 __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_constant__ PagedAttnParams p) {
     using C = BlockCfg<D>;
@@ -99,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
         }
         mbar_init(q_full, 4);
         mbar_init(q_free, 8);
-        mbar_init(q_staged, 32);
+        mbar_init(q_staged, 64);
         abort_s = 0;
         fence_mbar_init();
         tma_prefetch_desc(&p.tmap_half);
@@ -139,30 +158,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
         const int bl = p.table ? min(p.ps_log2, 6) : 6;          // log2 rows of a box
         const int box_rows = 1 << bl, boxes = 64 >> bl;
         const int b = lane & (boxes - 1), h = lane / boxes;       // this lane's box and 64-column half
-        int it = 0, seg = 0;
+        Stretch nx;
+        bool more = walk.next(line, nx);
+        int it = 0;
         bool ok = true;
-        for (; ok && walk.next(line, s); ++seg) {
+        for (int seg = 0; ok && more; ++seg) {
+            s = nx;
+            more = walk.next(line, nx);
+            int staged = more ? 0 : 128;      // vectors of the next stretch's Q this producer has seen to
+            // A few of them after each tile, every other eight by each producer, once the softmax has
+            // taken this stretch's Q from there.
+            auto stage_some = [&](int until) {
+                for (; staged < until; staged += 16)
+                    stage_q<D>(p, line, nx, q_stage, staged + kind * 8, staged + kind * 8 + 8, lane, 32);
+            };
             const int4 e = line.ent[s.i];
             const int hi = p.causal ? e.w + s.r1 : e.w + e.z;
             const int lo = p.window > 0 ? max(0, e.w + s.r0 - p.window + 1) : 0;
-            if (kind == 0) {
-                // the stretch's Q, whole rows per group of lanes (a softmax lane that read its own
-                // 256-byte row from global memory touched 32 lines per load: 2500 cycles; one bulk
-                // copy per row took 7000); the softmax has taken the one before
-                if (seg > 0) ok = mbar_wait_short(q_full, (uint32_t)((seg - 1) & 1), abort_flag, p.wait_status);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                const int nvec = (s.r1 - s.r0) * p.G, c = lane % (D / 8) * 8;
-                const __nv_bfloat16* src = (const __nv_bfloat16*)p.q + (size_t)(e.y + s.r0) * p.q_stride + s.g * p.G * D + c;
-                const uint32_t dst = smem_u32(q_stage) + c * 2;
-#pragma unroll 4
-                for (int v = lane / (D / 8); v < nvec; v += 256 / D) {
-                    const int r = v * p.g_magic >> 16, x = v - r * p.G;
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
-                                 ::"r"(dst + v * C::QLD), "l"((uint64_t)(src + r * p.q_stride + x * D)) : "memory");
-                }
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(q_staged)) : "memory");
-            }
             PageLookup look;
             look.reset();
             for (int t = s.t0; t < s.t1; ++t, ++it) {
@@ -187,6 +199,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                           "r"(0), "r"((int)row), "r"(h), "r"(smem_u32(&full[st]))
                         : "memory");
                 }
+                // (with S tiles issued since, the first tile's S is done, and so Q was taken)
+                if (t - s.t0 >= S && staged < 128) stage_some(staged + 16);
+            }
+            if (more && ok) {
+                ok = __all_sync(0xffffffffu, mbar_wait_short(q_full, (uint32_t)(seg & 1), abort_flag, p.wait_status));
+                if (!ok) break;
+                stage_some(128);
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(q_staged)) : "memory");
             }
         }
         if (!ok) {
@@ -275,8 +295,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
         // the lane's vector of stretch n (staged by the producer) into the Q operand; lanes past the
         // tile's vectors take whatever stands there (their rows are not written)
         auto put_q = [&](int n) -> bool {
-            bool got = mbar_wait_short(q_staged, (uint32_t)(n & 1), abort_flag, p.wait_status);
-            if (!__all_sync(0xffffffffu, got)) return false;
+            if (n > 0) {
+                const bool got = mbar_wait_short(q_staged, (uint32_t)((n - 1) & 1), abort_flag, p.wait_status);
+                if (!__all_sync(0xffffffffu, got)) return false;
+            }
             const uint8_t* src = q_stage + row * C::QLD;
 #pragma unroll 1
             for (int c0 = 0; c0 < D / 2; c0 += 16) {
@@ -307,7 +329,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
         }
         int it0 = 0, seg = 0;             // tiles and stretches before this one
         bool ok = true;
-        if (more && w == 0) ok = put_q(0);
+        if (more) {                       // the first stretch's Q: staged by all softmax threads
+            stage_q<D>(p, line, nx, q_stage, 0, 128, e256, kSoftmax);
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            named_bar_sync(1, kSoftmax);
+            if (w == 0) ok = put_q(0);
+        }
         while (more) {               // left by all threads together
             s = nx;
             const int4 e = line.ent[s.i];
