@@ -1,6 +1,8 @@
 // The paged key/value pool: views, launchers of the page operations (pages.cu)
 // and of attention over pages or over a cache slab (paged_attn.cu, paged_attn_tc.cu).
 #pragma once
+#include <atomic>
+
 #include "common.cuh"
 
 namespace df {
@@ -489,6 +491,19 @@ struct PageLookup {
 // Tensor map of a bf16 slab of `rows` rows of d elements for the kernels (abi.cu); false
 // when the driver's encoder rejects it.
 bool encode_kv_rows(CUtensorMap* m, const void* slab, uint64_t rows, int d, int box_rows, int halves);
+
+// Let a kernel use `bytes` of dynamic shared memory, once per kernel (ID: one number per
+// kernel) and device.
+template <int ID> bool allow_smem(const void* fn, int bytes) {
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return true;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    if (dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
 
 size_t paged_scratch_bytes();    // partials and counters of an attention launch
 constexpr size_t kPagedCounterBytes = 8192;

@@ -246,7 +246,7 @@ template <typename T, int D>
 int launch_simt(PagedAttnParams& p, int num_sms, cudaStream_t st) {
     const int smem = F32Smem<T>::bytes(D);
     auto kern = k_paged_attn_simt<T, D>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return 1;
+    if (!allow_smem<D * 8 + 7>((const void*)kern, smem)) return 1;
     const long long vbs = ((long long)p.max_rows * p.G + kVec - 1) / kVec;
     const long long items = vbs * p.nkv * p.n;
     // two blocks' worth of items per SM, no item split into less than its tiles

@@ -28,7 +28,7 @@ namespace df {
 
 namespace {
 
-constexpr int kOverhead = 4;   // units that starting and ending an item costs, in tiles
+constexpr int kOverhead = 10;   // units that starting and ending an item costs, in tiles
 constexpr int kMinShare = 8;   // smallest share of a CTA, in units
 
 constexpr int kThreads = 384;
@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ Page
 template <int D, int CS>
 int launch_dc(const PagedAttnParams& p, int num_sms, cudaStream_t st) {
     auto kern = k_paged_block<D, CS>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, BlockCfg<D>::SMEM) != cudaSuccess) return 1;
+    if (!allow_smem<D * 8 + CS>((const void*)kern, BlockCfg<D>::SMEM)) return 1;
     const int ctas = std::min(num_sms, kPagedCtas), pieces = p.rt * p.G * (D / 8);
     cudaError_t e = launch_k(kern, dim3(ctas), dim3(kThreads), BlockCfg<D>::SMEM, st, p);
     if (e == cudaSuccess) e = launch_k(k_paged_join<D>, dim3(ctas, (pieces + 255) / 256), dim3(256), 0, st, p);

@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
 template <int D>
 int launch_d(const PagedAttnParams& p, int num_sms, cudaStream_t st) {
     auto kern = k_paged_decode<D>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DecodeCfg<D>::SMEM) != cudaSuccess) return 1;
+    if (!allow_smem<D * 8>((const void*)kern, DecodeCfg<D>::SMEM)) return 1;
     return (int)launch_k(kern, dim3(std::min(num_sms, kPagedCtas)), dim3(kThreads), DecodeCfg<D>::SMEM, st, p);
 }
 

@@ -16,7 +16,6 @@ current CUDA stream of the pool's device, and never synchronise (except :meth:`s
 """
 from __future__ import annotations
 
-import contextlib
 from typing import Optional
 
 import torch
@@ -24,7 +23,11 @@ import torch
 from . import dflash as D
 from .drafter import _DT, _aligned_empty
 
-_NO_GUARD = contextlib.nullcontext()
+# The current stream of a device as a cudaStream_t; the private call takes a tenth of the time
+# of building a Stream object, which a call on a few microseconds of work notices.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = torch.cuda.current_device
 
 
 class PagePool:
@@ -48,7 +51,8 @@ class PagePool:
         self._index = self.device.index
         with torch.cuda.device(self.device):
             self._buf, self.ptr = _aligned_empty(self.nbytes, self.device)
-            self.handle = D.dflash_pool_init(c, self.ptr, self.nbytes, self._stream())
+            self.handle = D.dflash_pool_init(c, self.ptr, self.nbytes, _raw_stream(self._index))
+        self._lib = D.lib()
         info = D.dflash_pool_get_info(self.handle)
         self.max_pages = info.max_pages
         base = self._buf.data_ptr()
@@ -63,11 +67,16 @@ class PagePool:
         self._slab_at = info.slab - base
 
     # -- helpers -----------------------------------------------------------------
-    def _stream(self) -> int:
-        return torch.cuda.current_stream(self._index).cuda_stream
-
-    def _guard(self):
-        return _NO_GUARD if torch.cuda.current_device() == self._index else torch.cuda.device(self._index)
+    def _run(self, fn, *args) -> None:
+        """fn(handle, *args, stream) with the pool's device current."""
+        index = self._index
+        if _current_device() == index:
+            st = fn(self.handle, *args, _raw_stream(index))
+        else:
+            with torch.cuda.device(index):
+                st = fn(self.handle, *args, _raw_stream(index))
+        if st:
+            raise D.DflashError(st, fn.__name__)
 
     def _ids(self, t: Optional[torch.Tensor], what: str, n: Optional[int] = None) -> Optional[int]:
         """The address of an int32 list on the pool's device (None stays None)."""
@@ -83,13 +92,16 @@ class PagePool:
         """Row stride in elements of a [rows, heads, head_dim] tensor whose rows are contiguous."""
         if t.dtype is not self.torch_dtype or t.get_device() != self._index:
             raise ValueError("%s: a %s tensor on %s is wanted" % (what, self.torch_dtype, self.device))
-        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != self.head_dim:
-            raise ValueError("%s: shape [rows, %d, %d] is wanted, not %s" % (what, heads, self.head_dim,
-                                                                           tuple(t.shape)))
+        shape = t.shape
+        if len(shape) != 3 or shape[1] != heads or shape[2] != self.head_dim:
+            raise ValueError("%s: shape [rows, %d, %d] is wanted, not %s" % (what, heads, self.head_dim, tuple(shape)))
+        width = heads * self.head_dim
+        if t.is_contiguous():
+            return width
         stride = t.stride()
-        if t.shape[0] and (stride[2] != 1 or (heads > 1 and stride[1] != self.head_dim)):
+        if stride[2] != 1 or (heads > 1 and stride[1] != self.head_dim):
             raise ValueError("%s: the rows have to be contiguous" % what)
-        return stride[0] if t.shape[0] > 1 else max(stride[0], heads * self.head_dim)
+        return stride[0] if shape[0] > 1 else width
 
     # -- state -------------------------------------------------------------------
     def slab(self) -> torch.Tensor:
@@ -101,8 +113,8 @@ class PagePool:
 
     def status(self) -> int:
         """Synchronise, then return and clear the pool's sticky device error."""
-        with self._guard():
-            return D.dflash_pool_status(self.handle, self._stream())
+        with torch.cuda.device(self._index):
+            return D.dflash_pool_status(self.handle, _raw_stream(self._index))
 
     def launch_count(self) -> int:
         return D.dflash_pool_launch_count(self.handle)
@@ -111,38 +123,33 @@ class PagePool:
         """Replace every length and table (counts are taken from them); see dflash_pool_set_tables."""
         a = self._ids(lens, "lens", self.max_seqs)
         b = self._ids(table, "table", self.max_seqs * self.max_pages)
-        with self._guard():
-            D.dflash_pool_set_tables(self.handle, a, b, self._stream())
+        self._run(self._lib.dflash_pool_set_tables, a, b)
 
     # -- pages -------------------------------------------------------------------
     def reserve(self, grow: torch.Tensor, seqs: Optional[torch.Tensor] = None) -> None:
         """Make the positions [len, len + grow[i]) of each sequence writable (copy on write)."""
         n = grow.numel()
         a, g = self._ids(seqs, "seqs", n), self._ids(grow, "grow")
-        with self._guard():
-            D.dflash_pages_reserve(self.handle, a, g, n, self._stream())
+        self._run(self._lib.dflash_pages_reserve, a, g, n)
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor, deep: bool = False) -> None:
         """dst[i] shares src[i]'s pages (deep: gets copies of them)."""
         n = src.numel()
         a, b = self._ids(src, "src"), self._ids(dst, "dst", n)
-        with self._guard():
-            D.dflash_pages_fork(self.handle, a, b, n, deep, self._stream())
+        self._run(self._lib.dflash_pages_fork, a, b, n, 1 if deep else 0)
 
     def free(self, seqs: Optional[torch.Tensor] = None, keep: Optional[torch.Tensor] = None) -> None:
         """Cut each sequence back to keep[i] positions (None: to nothing) and give its pages back."""
         n = seqs.numel() if seqs is not None else keep.numel() if keep is not None else self.max_seqs
         a, k = self._ids(seqs, "seqs"), self._ids(keep, "keep", n)
-        with self._guard():
-            D.dflash_pages_free(self.handle, a, k, n, self._stream())
+        self._run(self._lib.dflash_pages_free, a, k, n)
 
     def compact(self, used: Optional[torch.Tensor] = None) -> torch.Tensor:
         """Move the pages in use to 0..used-1; returns `used` (int32[1] on the device)."""
         if used is None:
             used = torch.empty(1, dtype=torch.int32, device=self.device)
         u = self._ids(used, "used", 1)
-        with self._guard():
-            D.dflash_pages_compact(self.handle, u, self._stream())
+        self._run(self._lib.dflash_pages_compact, u)
         return used
 
     def write(self, layer: int, k: torch.Tensor, v: torch.Tensor, seqs: Optional[torch.Tensor] = None,
@@ -157,30 +164,26 @@ class PagePool:
         a, s, c = self._ids(seqs, "seqs", n), self._ids(row_start, "row_start", n), self._ids(row_count, "row_count", n)
         if rows == 0:
             return
-        with self._guard():
-            D.dflash_pages_write(self.handle, a, n, layer, k.data_ptr(), v.data_ptr(), sk, s, c, rows,
-                                 rows if max_rows is None else max_rows, self._stream())
+        self._run(self._lib.dflash_pages_write, a, n, layer, k.data_ptr(), v.data_ptr(), sk, s, c, rows,
+                  rows if max_rows is None else max_rows)
 
     def advance(self, row_count: Optional[torch.Tensor] = None, seqs: Optional[torch.Tensor] = None) -> None:
         """len += row_count[i] (None: 1) for each sequence."""
         n = row_count.numel() if row_count is not None else seqs.numel() if seqs is not None else self.max_seqs
         a, c = self._ids(seqs, "seqs", n), self._ids(row_count, "row_count")
-        with self._guard():
-            D.dflash_pages_advance(self.handle, a, c, n, self._stream())
+        self._run(self._lib.dflash_pages_advance, a, c, n)
 
     def store(self, cache, seqs: Optional[torch.Tensor] = None, reqs: Optional[torch.Tensor] = None) -> None:
         """Append to each sequence the positions that its request of the draft cache has more."""
         n = self._pairs(cache, seqs, reqs)
         a, b = self._ids(seqs, "seqs", n), self._ids(reqs, "reqs", n)
-        with self._guard():
-            D.dflash_pages_store(self.handle, a, cache.handle, b, n, self._stream())
+        self._run(self._lib.dflash_pages_store, a, cache.handle, b, n)
 
     def load(self, cache, seqs: Optional[torch.Tensor] = None, reqs: Optional[torch.Tensor] = None) -> None:
         """Append to each request of the draft cache the positions that its sequence has more."""
         n = self._pairs(cache, seqs, reqs)
         a, b = self._ids(seqs, "seqs", n), self._ids(reqs, "reqs", n)
-        with self._guard():
-            D.dflash_pages_load(self.handle, a, cache.handle, b, n, self._stream())
+        self._run(self._lib.dflash_pages_load, a, cache.handle, b, n)
 
     def _pairs(self, cache, seqs, reqs) -> int:
         if cache.drafter.device != self.device:
@@ -210,18 +213,19 @@ class PagePool:
         stride = self._rows(q, self.n_q_heads, "q")
         rows = q.shape[0]
         if out is None:
-            out = torch.empty((rows, self.n_q_heads, self.head_dim), dtype=q.dtype, device=q.device)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
         elif out.dtype is not q.dtype or out.shape != q.shape or not out.is_contiguous() or \
                 out.get_device() != self._index:
             raise ValueError("out: a contiguous tensor like q is wanted")
-        n = self._entries(seqs, row_start, row_count, rows)
-        a, s, c = self._ids(seqs, "seqs", n), self._ids(row_start, "row_start", n), self._ids(row_count, "row_count", n)
-        if rows == 0:
-            return out
-        with self._guard():
-            D.dflash_paged_attention(self.handle, a, n, layer, q.data_ptr(), stride, s, c, rows,
-                                     rows if max_rows is None else max_rows, causal, window, sinks, out.data_ptr(),
-                                     self._stream())
+        if seqs is None and row_count is None and row_start is None:
+            n, a, s, c = rows, None, None, None
+        else:
+            n = self._entries(seqs, row_start, row_count, rows)
+            a, s = self._ids(seqs, "seqs", n), self._ids(row_start, "row_start", n)
+            c = self._ids(row_count, "row_count", n)
+        if rows:
+            self._run(self._lib.dflash_paged_attention, a, n, layer, q.data_ptr(), stride, s, c, rows,
+                      rows if max_rows is None else max_rows, 1 if causal else 0, window, sinks, out.data_ptr())
         return out
 
     def __del__(self):
