@@ -11,6 +11,19 @@ constexpr int kPoolMaxSeqs = 1024;      // the plan kernels hold one sequence pe
 constexpr int kPagedCtas = 160;         // most CTAs of an attention launch with partials (>= SMs of any B200)
 constexpr int kPagedRowsTc = 128;       // query rows of a tensor-core row tile
 
+// Let a kernel use `bytes` of dynamic shared memory, once per kernel (ID: one number per
+// kernel) and device.
+template <int ID> bool allow_smem(const void* fn, int bytes) {
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return true;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    if (dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
+
 // Device view of a pool.
 struct PoolView {
     int* status;
@@ -46,11 +59,11 @@ struct CacheView {
 };
 bool cache_view(const dflash_cache* c, CacheView& v);
 
-int launch_pool_set_tables(const PoolView& v, const int* lens, const int* table, cudaStream_t st);
+int launch_pool_set_tables(const PoolView& v, const int* lens, const int* table, cudaStream_t st, int* launches);
 int launch_pages_reserve(const PoolView& v, const int* seqs, const int* grow, int n, cudaStream_t st);
 int launch_pages_fork(const PoolView& v, const int* src, const int* dst, int n, int deep, cudaStream_t st);
 int launch_pages_free(const PoolView& v, const int* seqs, const int* keep, int n, cudaStream_t st);
-int launch_pages_compact(const PoolView& v, int* used, cudaStream_t st);
+int launch_pages_compact(const PoolView& v, int* used, cudaStream_t st, int* launches);
 int launch_pages_write(const PoolView& v, const int* seqs, int n, int layer, const void* k, const void* vv,
                        long long stride_bytes, const int* row_start, const int* row_count, int total_rows, int max_rows,
                        cudaStream_t st);
@@ -491,19 +504,6 @@ struct PageLookup {
 // Tensor map of a bf16 slab of `rows` rows of d elements for the kernels (abi.cu); false
 // when the driver's encoder rejects it.
 bool encode_kv_rows(CUtensorMap* m, const void* slab, uint64_t rows, int d, int box_rows, int halves);
-
-// Let a kernel use `bytes` of dynamic shared memory, once per kernel (ID: one number per
-// kernel) and device.
-template <int ID> bool allow_smem(const void* fn, int bytes) {
-    static std::atomic<unsigned long long> done{0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    const unsigned long long bit = 1ull << (dev & 63);
-    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return true;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
-    if (dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
-    return true;
-}
 
 size_t paged_scratch_bytes();    // partials and counters of an attention launch
 constexpr size_t kPagedCounterBytes = 8192;

@@ -196,7 +196,9 @@ int dflash_pool_set_tables(dflash_pool* p, const int32_t* lens, const int32_t* t
     const int e = check(p, 0);
     if (e) return e;
     if (!lens || !table) return DFLASH_INVALID_ARG;
-    return done(p, launch_pool_set_tables(p->v, lens, table, S(stream)), 3);
+    int launches = 0;
+    const int r = launch_pool_set_tables(p->v, lens, table, S(stream), &launches);
+    return done(p, r, launches);
 }
 
 int dflash_pages_reserve(dflash_pool* p, const int32_t* seqs, const int32_t* grow, int n, dflash_stream stream) {
@@ -226,7 +228,9 @@ int dflash_pages_compact(dflash_pool* p, int32_t* used, dflash_stream stream) {
     const int e = check(p, 0);
     if (e) return e;
     if (!used) return DFLASH_INVALID_ARG;
-    return done(p, launch_pages_compact(p->v, used, S(stream)), 3);
+    int launches = 0;
+    const int r = launch_pages_compact(p->v, used, S(stream), &launches);
+    return done(p, r, launches);
 }
 
 int dflash_pages_write(dflash_pool* p, const int32_t* seqs, int n, int layer, const void* k, const void* v,

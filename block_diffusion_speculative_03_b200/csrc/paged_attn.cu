@@ -37,11 +37,6 @@ template <> DF_DEV void load4<float>(const float* p, float* v) {
     const float4 f = *reinterpret_cast<const float4*>(p);
     v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
 }
-template <> DF_DEV void load4<__nv_bfloat16>(const __nv_bfloat16* p, float* v) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
-    v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
-}
 
 // Grid: (vector blocks * nkv * splits, entries).
 template <typename T, int D>

@@ -15,7 +15,8 @@
 //   warp 0     TMA: K and V boxes of min(page_size, 64) rows (both 64-column halves of a
 //              row group in one box) into a ring; pages are looked up 32 at a time.
 //              Boxes in which no row sees a key are not loaded.
-//   warps 1-4  16 keys of every tile each, with their own running state: S = Q K^T and
+//   warps 1-8  two groups of four that take the tiles in turn, 16 keys of a tile per warp, with
+//              their own running state: S = Q K^T and
 //              O += P V on m16n8k16 tensor instructions, P staying in registers (the
 //              accumulator layout of S is the operand layout of P).  No barrier between
 //              the warps until the end of the item.  (At 16 rows the tensor work is 1/8 of
@@ -29,15 +30,15 @@ namespace df {
 
 namespace {
 
-constexpr int kThreads = 160;
-constexpr int kConsumers = 4;
+constexpr int kConsumers = 8;      // two groups of four warps take the tiles in turn
+constexpr int kThreads = 32 + 32 * kConsumers;
 constexpr int kTileKeys = kLineTile;
 constexpr int kOverhead = 2;   // units that starting and joining an item costs, in tiles
 constexpr int kMinShare = 4;   // smallest share of a CTA, in units
 
 template <int D> struct DecodeCfg {
     static constexpr int TILE = kTileKeys * D * 2;           // bytes of a K (or V) tile
-    static constexpr int STAGES = D == 128 ? 5 : 10;
+    static constexpr int STAGES = D == 128 ? 4 : 8;
     static constexpr int RING = STAGES * 2 * TILE;
     static constexpr int OLD = D + 4;                        // row stride of the join buffer (floats)
     static constexpr int JOIN = kConsumers * 16 * OLD * 4;
@@ -85,7 +86,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], kConsumers);
+            mbar_init(&empty[i], kConsumers / 2);
         }
         abort_s = 0;
         fence_mbar_init();
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
     }
 
     // ---------------------------------------------------------------- consumers
-    const int cw = warp - 1, c_tid = tid - 32;
+    const int cw = (warp - 1) & 3, group = (warp - 1) >> 2, jw = warp - 1, c_tid = tid - 32;
     const int qr = lane >> 2, qc = (lane & 3) * 2;            // accumulator row and first column of this lane
     // ldmatrix row of this lane: K: matrices (keys 0-7, 8 columns), (keys 0-7, next 8), (keys 8-15, ..), ..;
     // V transposed: (keys 0-7, columns), (keys 8-15, columns), (keys 0-7, next 8), ..
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
     const uint32_t k_off = row_addr(kk), v_off = row_addr(vk), half = (uint32_t)box_rows * 128;
     const uint32_t ring_a = smem_u32(ring);
 
-    int it = 0;
+    int it0 = 0;                                              // tiles before this stretch
     bool ok = true;
     while (walk.next(line, s)) {
         const int4 e = line.ent[s.i];
@@ -185,8 +186,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
         for (int j = 0; j < NT8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
         float base_a = -INFINITY, base_b = -INFINITY, l_a = 0.f, l_b = 0.f;
 
-        for (int t = s.t0; t < s.t1; ++t, ++it) {
-            const int st = it % S;
+        for (int t = s.t0 + ((it0 ^ group) & 1); t < s.t1; t += 2) {
+            const int it = it0 + t - s.t0, st = it % S;
             if (ok) ok = mbar_wait_short(&full[st], (uint32_t)((it / S) & 1), abort_flag, p.wait_status);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) continue;
@@ -276,14 +277,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
         l_a += __shfl_xor_sync(0xffffffffu, l_a, 2);
         l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
         if ((lane & 3) == 0) {
-            join_ml[cw * 16 + qr] = make_float2(base_a, l_a);
-            join_ml[cw * 16 + qr + 8] = make_float2(base_b, l_b);
+            join_ml[jw * 16 + qr] = make_float2(base_a, l_a);
+            join_ml[jw * 16 + qr + 8] = make_float2(base_b, l_b);
         }
 #pragma unroll
         for (int j = 0; j < NT8; ++j) {
-            if (qr < R) *reinterpret_cast<float2*>(join + (cw * 16 + qr) * C::OLD + j * 8 + qc) = make_float2(o[j][0], o[j][1]);
+            if (qr < R) *reinterpret_cast<float2*>(join + (jw * 16 + qr) * C::OLD + j * 8 + qc) = make_float2(o[j][0], o[j][1]);
             if (qr + 8 < R)
-                *reinterpret_cast<float2*>(join + (cw * 16 + qr + 8) * C::OLD + j * 8 + qc) = make_float2(o[j][2], o[j][3]);
+                *reinterpret_cast<float2*>(join + (jw * 16 + qr + 8) * C::OLD + j * 8 + qc) = make_float2(o[j][2], o[j][3]);
         }
         named_bar_sync(1, kConsumers * 32);
         const bool whole = s.whole(), head = s.t0 == 0;   // head: holds the item's first tile
@@ -332,23 +333,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
                 auto part = [&](int c) { return p.partial + (size_t)(2 * c + (c == c0 ? 1 : 0)) * C::SLOT; };
                 for (int x = c_tid; x < R * (D / 4); x += kConsumers * 32) {
                     const int r = x / (D / 4), c = (x % (D / 4)) * 4;
-                    float B = -INFINITY;
-#pragma unroll 8
-                    for (int k = c0; k <= c1; ++k) B = fmaxf(B, __ldcg(part(k) + 2 * r));
-                    const float z = B == -INFINITY ? 0.f : B;
-                    float L = 0.f;
+                    float B = -INFINITY, L = 0.f;
                     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                    for (int k = c0; k <= c1; ++k) {
-                        const float* q = part(k);
-                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(q + 2 * r));
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(q + 32 + r * D + c));
-                        const float f = exp2f(ml.x - z);
-                        L += f * ml.y;
-                        a.x += f * v.x;
-                        a.y += f * v.y;
-                        a.z += f * v.z;
-                        a.w += f * v.w;
+                    for (int k0 = c0; k0 <= c1; k0 += 8) {      // eight partials' loads in flight
+                        float2 ml[8];
+                        float4 v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float* q = part(min(k0 + k, c1));
+                            ml[k] = __ldcg(reinterpret_cast<const float2*>(q + 2 * r));
+                            v[k] = __ldcg(reinterpret_cast<const float4*>(q + 32 + r * D + c));
+                        }
+                        float nb = B;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) nb = fmaxf(nb, ml[k].x);
+                        const float z = nb == -INFINITY ? 0.f : nb, g = exp2f(B - z);
+                        B = nb;
+                        L *= g;
+                        a.x *= g;
+                        a.y *= g;
+                        a.z *= g;
+                        a.w *= g;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            if (k0 + k > c1) break;
+                            const float f = exp2f(ml[k].x - z);
+                            L += f * ml[k].y;
+                            a.x += f * v[k].x;
+                            a.y += f * v[k].y;
+                            a.z += f * v[k].z;
+                            a.w += f * v[k].w;
+                        }
                     }
                     const float inv = L == 0.f ? 0.f : 1.0f / L;
                     __nv_bfloat16* dst = (__nv_bfloat16*)p.out + ((size_t)(e.y + r / p.G) * p.nq + (size_t)s.g * p.G + r % p.G) * D + c;
@@ -356,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
                 }
             }
         }
+        it0 += s.t1 - s.t0;
         named_bar_sync(1, kConsumers * 32);          // the join buffer and flag_s are free again
     }
 }

@@ -220,8 +220,10 @@ __global__ void __launch_bounds__(kPlan) k_pages_plan(PoolView v, const int* __r
 // ---------------------------------------------------------------------------
 // Copies of pages
 // ---------------------------------------------------------------------------
-// Unit: up to 4 KB of one (layer, kind, head) run of one copied page, one warp, its
-// eight 16-byte loads per lane issued before the first store.
+// Bound by HBM: every byte is read once and written once.
+//
+// Parts of pages (copy on write).  Unit: up to 4 KB of one (layer, kind, head) run of one
+// copied page, one warp, its eight 16-byte loads per lane issued before the first store.
 __global__ void __launch_bounds__(kCopyWarps * 32) k_pages_copy(PoolView v) {
     griddep_wait();
     griddep_launch();
@@ -249,6 +251,66 @@ __global__ void __launch_bounds__(kCopyWarps * 32) k_pages_copy(PoolView v) {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             if (lane + 32 * k < nv) __stcs(b + lane + 32 * k, r[k]);
+    }
+}
+
+// Whole pages (deep fork, compact): one warp per SM keeps kBulkStages chunks of 32 KB in flight
+// through shared memory with bulk copies, in and out; no registers, no address arithmetic
+// beside one record per chunk.  (The warp-per-4-KB kernel above on the same pages: 79 % of the
+// copy rate.)
+constexpr int kBulkStages = 6, kBulkChunk = 32768;
+__global__ void __launch_bounds__(32) k_pages_copy_whole(PoolView v) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = smem_align_up<uint8_t>(smem_raw, 128);
+    __shared__ uint64_t full[kBulkStages];
+    __shared__ int abort_s;
+    griddep_wait();
+    griddep_launch();
+    if (threadIdx.x != 0) return;
+    abort_s = 0;
+    for (int i = 0; i < kBulkStages; ++i) mbar_init(&full[i], 1);
+    fence_mbar_init();
+    const int cpp = (int)((v.page_bytes + kBulkChunk - 1) / kBulkChunk);      // chunks of a page
+    const long long chunks = (long long)*v.n_copies * cpp;
+    const long long mine = chunks > blockIdx.x ? (chunks - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+    const uint64_t once = make_l2_policy_evict_first();
+    auto place = [&](long long i, size_t& from, size_t& to) -> uint32_t {
+        const long long u = blockIdx.x + i * gridDim.x;
+        const int4 rec = v.copies[u / cpp];
+        const long long o = (u % cpp) * kBulkChunk;
+        from = (size_t)rec.x * v.page_bytes + o;
+        to = (size_t)rec.y * v.page_bytes + o;
+        return (uint32_t)min((long long)kBulkChunk, v.page_bytes - o);
+    };
+    auto load = [&](long long i) {
+        size_t from, to;
+        const uint32_t n = place(i, from, to);
+        const int st = (int)(i % kBulkStages);
+        mbar_arrive_expect_tx(&full[st], n);
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
+                     ::"r"(smem_u32(ring + st * kBulkChunk)), "l"((uint64_t)(v.slab + from)), "r"(n), "r"(smem_u32(&full[st])),
+                       "l"(once)
+                     : "memory");
+    };
+    for (long long i = 0; i < kBulkStages && i < mine; ++i) load(i);
+    for (long long i = 0; i < mine; ++i) {
+        const int st = (int)(i % kBulkStages);
+        if (!mbar_wait(&full[st], (uint32_t)((i / kBulkStages) & 1), &abort_s, v.status)) break;
+        size_t from, to;
+        const uint32_t n = place(i, from, to);
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group.L2::cache_hint [%0], [%1], %2, %3;"
+                     ::"l"((uint64_t)(v.slab + to)), "r"(smem_u32(ring + st * kBulkChunk)), "r"(n), "l"(once) : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        if (i >= 1 && i - 1 + kBulkStages < mine) {
+            // the stage of the chunk before is free once its store has read it
+            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            load(i - 1 + kBulkStages);
+        }
+    }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (abort_s) {      // copies in land before the block exits
+        volatile int never = 0;
+        for (int k = 0; k < kBulkStages; ++k) mbar_wait(&full[k], 0, &never, nullptr);
     }
 }
 
@@ -314,7 +376,7 @@ __global__ void k_pages_free(PoolView v, const int* __restrict__ seqs, const int
 // ---------------------------------------------------------------------------
 // compact
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(kPlan) k_pages_compact(PoolView v, int* __restrict__ used_out) {
+__global__ void __launch_bounds__(kPlan) k_pages_compact(PoolView v, int* __restrict__ used_out, int remap) {
     __shared__ int sums[33];
     griddep_wait();
     griddep_launch();
@@ -365,6 +427,12 @@ __global__ void __launch_bounds__(kPlan) k_pages_compact(PoolView v, int* __rest
         v.n_copies[1] = used;
         *used_out = used;
     }
+    if (!remap || moves == 0) return;
+    __syncthreads();
+    for (int e = t; e < v.max_seqs * v.max_pages; e += kPlan) {
+        const int x = v.table[e];
+        if (x >= used) v.table[e] = v.movers[x];
+    }
 }
 
 __global__ void k_pages_remap(PoolView v) {
@@ -391,27 +459,24 @@ __global__ void k_tables_begin(PoolView v) {
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) v.n_copies[2] = 0;
 }
+// Whether table entry e can stand; counts its page.
+DF_DEV bool count_entry(const PoolView& v, const int* lens, const int* table, size_t e) {
+    const int s = (int)(e / v.max_pages), c = (int)(e % v.max_pages);
+    const int ln = lens[s], x = table[e];
+    if (ln < 0 || ln > v.max_len || x < -1 || x >= v.n_pages) return false;
+    if (x < 0) return c >= pages_for(ln, v.ps_log2);
+    if (c > 0 && table[e - 1] < 0) return false;
+    const int at = atomicCAS(&v.movers[x], -1, c);
+    atomicAdd(&v.refs[x], 1);
+    return at == -1 || at == c;
+}
 __global__ void k_tables_count(PoolView v, const int* lens, const int* table) {
     griddep_wait();
     griddep_launch();
     const size_t n = (size_t)v.max_seqs * v.max_pages;
     bool bad = false;
-    for (size_t e = (size_t)blockIdx.x * blockDim.x + threadIdx.x; e < n; e += (size_t)gridDim.x * blockDim.x) {
-        const int s = (int)(e / v.max_pages), c = (int)(e % v.max_pages);
-        const int ln = lens[s], x = table[e];
-        if (ln < 0 || ln > v.max_len || x < -1 || x >= v.n_pages) {
-            bad = true;
-            continue;
-        }
-        if (x < 0) {
-            bad |= c < pages_for(ln, v.ps_log2);
-            continue;
-        }
-        bad |= c > 0 && table[e - 1] < 0;
-        const int at = atomicCAS(&v.movers[x], -1, c);
-        bad |= at != -1 && at != c;
-        atomicAdd(&v.refs[x], 1);
-    }
+    for (size_t e = (size_t)blockIdx.x * blockDim.x + threadIdx.x; e < n; e += (size_t)gridDim.x * blockDim.x)
+        bad |= !count_entry(v, lens, table, e);
     if (bad) v.n_copies[2] = 1;
 }
 __global__ void k_tables_apply(PoolView v, const int* lens, const int* table) {
@@ -424,6 +489,29 @@ __global__ void k_tables_apply(PoolView v, const int* lens, const int* table) {
     for (size_t s = t; s < (size_t)v.max_seqs; s += step) v.len[s] = bad ? 0 : lens[s];
     if (bad) {
         for (size_t i = t; i < (size_t)v.n_pages; i += step) v.refs[i] = 0;
+        if (t == 0) set_error(v.status, DFLASH_INVALID_ARG);
+    }
+}
+
+// The three steps in one block, for tables that it goes through faster than two more launches
+// take (4096 entries: 5 us against 8; 10000: 15).
+constexpr int kSmallTables = 4096;
+__global__ void __launch_bounds__(kPlan) k_tables_small(PoolView v, const int* lens, const int* table) {
+    griddep_wait();
+    griddep_launch();
+    const int t = threadIdx.x, n = v.max_seqs * v.max_pages;
+    for (int i = t; i < v.n_pages; i += kPlan) {
+        v.refs[i] = 0;
+        v.movers[i] = -1;
+    }
+    __syncthreads();
+    bool bad = false;
+    for (int e = t; e < n; e += kPlan) bad |= !count_entry(v, lens, table, e);
+    bad = __syncthreads_or(bad);
+    for (int e = t; e < n; e += kPlan) v.table[e] = bad ? -1 : table[e];
+    if (t < v.max_seqs) v.len[t] = bad ? 0 : lens[t];
+    if (bad) {
+        for (int i = t; i < v.n_pages; i += kPlan) v.refs[i] = 0;
         if (t == 0) set_error(v.status, DFLASH_INVALID_ARG);
     }
 }
@@ -585,12 +673,22 @@ int copy_blocks(const PoolView& v, long long most_copies) {
     const long long b = (most_copies * per + kCopyWarps - 1) / kCopyWarps;
     return (int)(b < 1 ? 1 : b > 148 * 8 ? 148 * 8 : b);
 }
+cudaError_t copy_whole(const PoolView& v, cudaStream_t st) {
+    constexpr int smem = kBulkStages * kBulkChunk + 128;
+    if (!allow_smem<1>((const void*)k_pages_copy_whole, smem)) return cudaErrorInvalidValue;
+    return launch_k(k_pages_copy_whole, dim3(148), dim3(32), smem, st, v);
+}
 int blocks_for(size_t n) { return (int)(n + 255 < 256 * 592 ? (n + 255) / 256 : 592); }
 
 }  // namespace
 
-int launch_pool_set_tables(const PoolView& v, const int* lens, const int* table, cudaStream_t st) {
+int launch_pool_set_tables(const PoolView& v, const int* lens, const int* table, cudaStream_t st, int* launches) {
     const size_t n = (size_t)v.max_seqs * v.max_pages;
+    if (n <= kSmallTables && v.n_pages <= kSmallTables) {
+        *launches = 1;
+        return (int)launch_k(k_tables_small, dim3(1), dim3(kPlan), 0, st, v, lens, table);
+    }
+    *launches = 3;
     cudaError_t e = launch_k(k_tables_begin, dim3(blocks_for(v.n_pages)), dim3(256), 0, st, v);
     if (e == cudaSuccess) e = launch_k(k_tables_count, dim3(blocks_for(n)), dim3(256), 0, st, v, lens, table);
     if (e == cudaSuccess) e = launch_k(k_tables_apply, dim3(blocks_for(n)), dim3(256), 0, st, v, lens, table);
@@ -606,7 +704,7 @@ int launch_pages_reserve(const PoolView& v, const int* seqs, const int* grow, in
 int launch_pages_fork(const PoolView& v, const int* src, const int* dst, int n, int deep, cudaStream_t st) {
     if (!deep) return (int)launch_k(k_pages_fork, dim3(n), dim3(256), 0, st, v, src, dst);
     cudaError_t e = launch_k(k_pages_plan<true>, dim3(1), dim3(kPlan), 0, st, v, dst, (const int*)nullptr, src, n);
-    if (e == cudaSuccess) e = launch_k(k_pages_copy, dim3(copy_blocks(v, v.n_pages)), dim3(kCopyWarps * 32), 0, st, v);
+    if (e == cudaSuccess) e = copy_whole(v, st);
     return (int)e;
 }
 
@@ -614,11 +712,14 @@ int launch_pages_free(const PoolView& v, const int* seqs, const int* keep, int n
     return (int)launch_k(k_pages_free, dim3(n), dim3(256), 0, st, v, seqs, keep);
 }
 
-int launch_pages_compact(const PoolView& v, int* used, cudaStream_t st) {
-    cudaError_t e = launch_k(k_pages_compact, dim3(1), dim3(kPlan), 0, st, v, used);
-    if (e == cudaSuccess)
+int launch_pages_compact(const PoolView& v, int* used, cudaStream_t st, int* launches) {
+    // small tables are followed up by the planning block itself
+    const bool small = (size_t)v.max_seqs * v.max_pages <= kSmallTables;
+    *launches = small ? 2 : 3;
+    cudaError_t e = launch_k(k_pages_compact, dim3(1), dim3(kPlan), 0, st, v, used, small ? 1 : 0);
+    if (e == cudaSuccess && !small)
         e = launch_k(k_pages_remap, dim3(blocks_for((size_t)v.max_seqs * v.max_pages)), dim3(256), 0, st, v);
-    if (e == cudaSuccess) e = launch_k(k_pages_copy, dim3(copy_blocks(v, v.n_pages)), dim3(kCopyWarps * 32), 0, st, v);
+    if (e == cudaSuccess) e = copy_whole(v, st);
     return (int)e;
 }
 
