@@ -302,7 +302,8 @@ struct Stretch {
     int v0;             // the item's first unit
     DF_DEV bool whole() const { return t0 == 0 && t1 == span.nt; }
 };
-struct Walker {
+// TILES: entries may have several row tiles.
+template <bool TILES> struct Walker {
     int v, end;         // units still to come
     int i, t, g, off;   // item and units of it that lie before v
     int T;              // row tiles of entry i
@@ -327,10 +328,16 @@ struct Walker {
         }
         int local = v - L.pre[i];
         const int4 e = L.ent[i];
-        T = L.row_tiles(i);
         t = 0;
-        int size = L.span(e, 0).nt + L.ovh;
-        if (T > 1) {
+        T = 1;
+        int size;
+        if constexpr (!TILES) {
+            size = (L.pre[i + 1] - L.pre[i]) / L.nkv;
+        } else {
+            T = L.row_tiles(i);
+            size = L.span(e, 0).nt + L.ovh;
+        }
+        if (TILES && T > 1) {
             for (int tb = 0;; tb += 32) {
                 const int tt = tb + lane;
                 const int sz = tt < T ? L.span(e, tt).nt + L.ovh : 0;
@@ -358,8 +365,8 @@ struct Walker {
     DF_DEV bool next(const Line& L, Stretch& s) {
         while (v < end) {
             const int4 e = L.ent[i];
-            s.r0 = t * L.rt;
-            s.r1 = min(e.z, s.r0 + L.rt);
+            s.r0 = TILES ? t * L.rt : 0;
+            s.r1 = TILES ? min(e.z, s.r0 + L.rt) : e.z;
             s.span = key_span(e.w, e.z, s.r0, s.r1, L.causal, L.window, L.sinks, kLineTile);
             const int size = s.span.nt + L.ovh;
             const int take = min(size - off, end - v);
@@ -374,10 +381,10 @@ struct Walker {
                 off = 0;
                 if (++g == L.nkv) {
                     g = 0;
-                    if (++t >= T) {
+                    if (!TILES || ++t >= T) {
                         t = 0;
                         while (++i < L.n && L.ent[i].z == 0) {}
-                        if (i < L.n) T = L.row_tiles(i);
+                        if (TILES && i < L.n) T = L.row_tiles(i);
                     }
                 }
             }
@@ -414,6 +421,13 @@ DF_DEV bool mbar_wait_short(uint64_t* bar, uint32_t parity, volatile int* abort_
         }
     }
 }
+DF_DEV int atom_add_acq_rel(int* p, int v) {
+    int old;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
+}
+// 2^x for an integer x <= 0 (0 below -126), exactly; bases differ by integers.
+DF_DEV float pow2_int(float x) { return __int_as_float(((int)fmaxf(x, -127.f) + 127) << 23); }
 // Arrive without a branch.
 DF_DEV void mbar_arrive_if(bool pred, uint64_t* bar) {
     asm volatile(

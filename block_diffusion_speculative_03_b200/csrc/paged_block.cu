@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
     const int P = min((int)gridDim.x, max(1, U / kMinShare));
     if (tid == 64) rec[0] = make_int4(-1, 0, 0, 0);      // no item to join from here, so far
     if (U == 0 || (int)blockIdx.x >= P) return;
-    Walker walk;
+    Walker<true> walk;
     walk.start(line, line_begin(blockIdx.x, U, P), line_begin(blockIdx.x + 1, U, P));
     Stretch s;
     uint32_t tmem = 0;
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                 tc_fence_after();
                 if (__any_sync(0xffffffffu, grow)) {
                     if (t >= s.t0 + 2) {   // O holds earlier tiles
-                        const float f = grow ? exp2f(base - nb - kBaseLead) : 1.0f;
+                        const float f = grow ? pow2_int(base - nb - kBaseLead) : 1.0f;
 #pragma unroll 1
                         for (int c0 = 0; c0 < D; c0 += 32) {
                             float v[32];
@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                 constexpr int HC = D / 2;
                 const float2 m0 = ml[rl], m1 = ml[128 + rl];
                 const float B = fmaxf(m0.x, m1.x), z = B == -INFINITY ? 0.f : B;
-                const float g0 = exp2f(m0.x - z), g1 = exp2f(m1.x - z), f0 = w ? g1 : g0;
+                const float g0 = pow2_int(m0.x - z), g1 = pow2_int(m1.x - z), f0 = w ? g1 : g0;
                 const float L = g0 * m0.y + g1 * m1.y, inv = L == 0.f ? 0.f : 1.0f / L;
                 float* mine = join + (w * 128 + rl) * C::HLD;
                 float* theirs = join + ((w ^ 1) * 128 + rl) * C::HLD;
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                 if (w == 0) {
                     const float2 other = ml[128 + rl];
                     const float B = fmaxf(base, other.x), z = B == -INFINITY ? 0.f : B;
-                    const float f0 = exp2f(base - z), f1 = exp2f(other.x - z);
+                    const float f0 = pow2_int(base - z), f1 = pow2_int(other.x - z);
 #pragma unroll 1
                     for (int c0 = 0; c0 < D; c0 += 32) {
                         float v[32];
@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
 #pragma unroll
                     for (int k = 0; k < CS; ++k) {
                         const float2 m = ml[v + k * RW];
-                        const float f = exp2f(m.x - z);
+                        const float f = pow2_int(m.x - z);
                         const float4 w0 = *reinterpret_cast<const float4*>(join + (v + k * RW) * C::OLD + c);
                         const float4 w1 = *reinterpret_cast<const float4*>(join + (v + k * RW) * C::OLD + c + 4);
                         L += f * m.y;
@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ Page
 #pragma unroll
         for (int k = 0; k < 4; ++k) nb = fmaxf(nb, m[k].x);
         const float z = nb == -INFINITY ? 0.f : nb;
-        const float f0 = exp2f(B - z);
+        const float f0 = pow2_int(B - z);
         B = nb;
         L *= f0;
 #pragma unroll
@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ Page
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             if (k0 + k > rec.x) break;
-            const float f = exp2f(m[k].x - z);
+            const float f = pow2_int(m[k].x - z);
             L += f * m[k].y;
             a[0] += f * w0[k].x; a[1] += f * w0[k].y; a[2] += f * w0[k].z; a[3] += f * w0[k].w;
             a[4] += f * w1[k].x; a[5] += f * w1[k].y; a[6] += f * w1[k].z; a[7] += f * w1[k].w;

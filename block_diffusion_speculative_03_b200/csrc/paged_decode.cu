@@ -34,7 +34,7 @@ constexpr int kConsumers = 8;      // two groups of four warps take the tiles in
 constexpr int kThreads = 32 + 32 * kConsumers;
 constexpr int kTileKeys = kLineTile;
 constexpr int kOverhead = 2;   // units that starting and joining an item costs, in tiles
-constexpr int kMinShare = 4;   // smallest share of a CTA, in units
+constexpr int kMinShare = 3;   // smallest share of a CTA, in units
 
 template <int D> struct DecodeCfg {
     static constexpr int TILE = kTileKeys * D * 2;           // bytes of a K (or V) tile
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
     const int U = line_plan<kThreads, D>(p, line, line_mem, sums, kOverhead);
     const int P = min((int)gridDim.x, max(1, U / kMinShare));
     if (U == 0 || (int)blockIdx.x >= P) return;
-    Walker walk;
+    Walker<false> walk;
     walk.start(line, line_begin(blockIdx.x, U, P), line_begin(blockIdx.x + 1, U, P));
     Stretch s;
     const int bl = p.table ? min(p.ps_log2, 6) : 6;          // log2 rows of a TMA box
@@ -165,14 +165,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
         const int4 e = line.ent[s.i];
         const int R = e.z * p.G, hi = e.w + e.z, lo = p.window > 0 ? max(0, e.w - p.window + 1) : 0;
         // this lane's two rows: vector v = row * G + head
-        const int ra = qr / p.G, rb = (qr + 8) / p.G;
+        const int ra = qr * p.g_magic >> 16, rb = (qr + 8) * p.g_magic >> 16;
         const int pos_a = e.w + ra, pos_b = e.w + rb;
         const int hi_a = qr < R ? (p.causal ? pos_a + 1 : hi) : 0, hi_b = qr + 8 < R ? (p.causal ? pos_b + 1 : hi) : 0;
         uint32_t qf[D / 16][4];
         {
             const __nv_bfloat16* q = (const __nv_bfloat16*)p.q;
-            const __nv_bfloat16* qa = q + (size_t)(e.y + ra) * p.q_stride + (size_t)(s.g * p.G + qr % p.G) * D + qc;
-            const __nv_bfloat16* qb = q + (size_t)(e.y + rb) * p.q_stride + (size_t)(s.g * p.G + (qr + 8) % p.G) * D + qc;
+            const __nv_bfloat16* qa = q + (size_t)(e.y + ra) * p.q_stride + (size_t)(s.g * p.G + qr - ra * p.G) * D + qc;
+            const __nv_bfloat16* qb = q + (size_t)(e.y + rb) * p.q_stride + (size_t)(s.g * p.G + qr + 8 - rb * p.G) * D + qc;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 qf[k][0] = qr < R ? *reinterpret_cast<const uint32_t*>(qa + k * 16) : 0u;
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
                 xb = floorf(fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 2)));
                 const float na = xa > base_a + kBaseLag ? xa + kBaseLead : base_a;
                 const float nb = xb > base_b + kBaseLag ? xb + kBaseLead : base_b;
-                const float fa = na == base_a ? 1.f : exp2f(base_a - na), fb = nb == base_b ? 1.f : exp2f(base_b - nb);
+                const float fa = na == base_a ? 1.f : pow2_int(base_a - na), fb = nb == base_b ? 1.f : pow2_int(base_b - nb);
                 base_a = na;
                 base_b = nb;
                 l_a *= fa;
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
 #pragma unroll
             for (int w = 0; w < kConsumers; ++w) {
                 const float2 ml = join_ml[w * 16 + r];
-                const float f = exp2f(ml.x - z);
+                const float f = pow2_int(ml.x - z);
                 const float4 v = *reinterpret_cast<const float4*>(join + (w * 16 + r) * C::OLD + c);
                 L += f * ml.y;
                 a.x += f * v.x;
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
             }
             if (whole) {
                 const float inv = L == 0.f ? 0.f : 1.0f / L;
-                __nv_bfloat16* dst = (__nv_bfloat16*)p.out + ((size_t)(e.y + r / p.G) * p.nq + (size_t)s.g * p.G + r % p.G) * D + c;
+                __nv_bfloat16* dst = (__nv_bfloat16*)p.out + ((size_t)(e.y + (r * p.g_magic >> 16)) * p.nq + (size_t)s.g * p.G + r - (r * p.g_magic >> 16) * p.G) * D + c;
                 *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
             } else {
                 *reinterpret_cast<float4*>(slot + 32 + r * D + c) = a;
@@ -320,16 +320,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
         if (!whole) {
             // the CTAs that hold the item's first and last tile
             const int c0 = line_owner(s.v0 + kOverhead, U, P), c1 = line_owner(s.v0 + kOverhead + s.span.nt - 1, U, P);
-            __threadfence();
             named_bar_sync(1, kConsumers * 32);
             if (c_tid == 0) {
-                const int before = atomicAdd(&p.counters[c0], 1);
+                // releases the block's partial (the barrier above) and acquires the others'
+                const int before = atom_add_acq_rel(&p.counters[c0], 1);
                 flag_s = before == c1 - c0;
                 if (before == c1 - c0) p.counters[c0] = 0;      // ready for the next launch
             }
             named_bar_sync(1, kConsumers * 32);
             if (flag_s) {
-                __threadfence();
                 auto part = [&](int c) { return p.partial + (size_t)(2 * c + (c == c0 ? 1 : 0)) * C::SLOT; };
                 for (int x = c_tid; x < R * (D / 4); x += kConsumers * 32) {
                     const int r = x / (D / 4), c = (x % (D / 4)) * 4;
@@ -347,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
                         float nb = B;
 #pragma unroll
                         for (int k = 0; k < 8; ++k) nb = fmaxf(nb, ml[k].x);
-                        const float z = nb == -INFINITY ? 0.f : nb, g = exp2f(B - z);
+                        const float z = nb == -INFINITY ? 0.f : nb, g = pow2_int(B - z);
                         B = nb;
                         L *= g;
                         a.x *= g;
@@ -357,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
                             if (k0 + k > c1) break;
-                            const float f = exp2f(ml[k].x - z);
+                            const float f = pow2_int(ml[k].x - z);
                             L += f * ml[k].y;
                             a.x += f * v[k].x;
                             a.y += f * v[k].y;
@@ -366,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
                         }
                     }
                     const float inv = L == 0.f ? 0.f : 1.0f / L;
-                    __nv_bfloat16* dst = (__nv_bfloat16*)p.out + ((size_t)(e.y + r / p.G) * p.nq + (size_t)s.g * p.G + r % p.G) * D + c;
+                    __nv_bfloat16* dst = (__nv_bfloat16*)p.out + ((size_t)(e.y + (r * p.g_magic >> 16)) * p.nq + (size_t)s.g * p.G + r - (r * p.g_magic >> 16) * p.G) * D + c;
                     *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
                 }
             }
