@@ -6,13 +6,14 @@
 //
 // One block of 4 warps takes up to 8 query vectors of one (entry, kv head): the vectors
 // v = row * G + head of the entry, in order, share every key and value that is read.  A
-// warp walks 32-key tiles: it stages the K rows in its part of shared memory, each lane
-// forms one key's dot products with the 8 vectors (K rows padded by 16 bytes, so the 32
-// lanes' 16-byte reads of one column hit all banks once), the weights go to shared
-// memory, and each lane accumulates its D / 32 columns of the output over the tile's V
-// rows, read straight from global memory.  The four warps' (m, l, o) are joined in shared
-// memory; with few items the keys are also split over `splits` blocks, whose partials the
-// last one to arrive joins in split order.
+// warp walks 32-key tiles through its part of shared memory: K of the next tile comes in
+// (asynchronous copies) while the values of this one are weighted, V while its scores are
+// formed.  Each lane forms one key's dot products with the 8 vectors (K rows padded by 16
+// bytes, so the 32 lanes' 16-byte reads of one column hit all banks once), the weights go to
+// shared memory, and each lane accumulates its D / 32 columns of the output over the tile's
+// V rows.  The four warps' (m, l, o) are joined in shared memory; with few items the keys are
+// also split over `splits` blocks, whose partials the last one to arrive joins in split order.
+// Bound by latency at few keys (two memory round trips per 32 keys of a warp), by HBM at many.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -21,31 +22,24 @@ namespace df {
 
 namespace {
 
-constexpr int kVec = 8;       // query vectors per block
 constexpr int kWarps = 4;
 constexpr int kTile = 32;     // keys of a warp's tile
 constexpr int kMaxSplits = 32;
 
-template <typename T> struct F32Smem {
-    static constexpr int bytes(int d) {
-        return kVec * d * 4 + kWarps * kTile * (d + 4) * 4 + kWarps * kVec * kTile * 4 + kWarps * kVec * 8;
-    }
-};
-
-template <typename T> DF_DEV void load4(const T* p, float* v);
-template <> DF_DEV void load4<float>(const float* p, float* v) {
-    const float4 f = *reinterpret_cast<const float4*>(p);
-    v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+constexpr int smem_bytes(int d, int kVec) {
+    return kVec * d * 4 + kWarps * kTile * (2 * d + 4) * 4 + kWarps * kVec * kTile * 4 + kWarps * kVec * 8;
 }
 
 // Grid: (vector blocks * nkv * splits, entries).
-template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) k_paged_attn_simt(const __grid_constant__ PagedAttnParams p) {
+// kVec: query vectors per block.
+template <int D, int kVec>
+__global__ void __launch_bounds__(kWarps * 32) k_paged_attn_f32(const __grid_constant__ PagedAttnParams p) {
     constexpr int C = D / 32;                   // output columns per lane
     extern __shared__ __align__(16) float sm[];
     float* sq = sm;                             // [kVec][D], scaled to log2 units
     float* sk = sq + kVec * D;                  // [kWarps][kTile][D + 4]
-    float* sp = sk + kWarps * kTile * (D + 4);  // [kWarps][kVec][kTile]
+    float* sv = sk + kWarps * kTile * (D + 4);  // [kWarps][kTile][D]
+    float* sp = sv + kWarps * kTile * D;        // [kWarps][kVec][kTile]
     float2* sml = reinterpret_cast<float2*>(sp + kWarps * kVec * kTile);   // [kWarps][kVec]
     __shared__ int last;
     griddep_wait();
@@ -58,28 +52,31 @@ __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_simt(const __grid_co
     const int nvec = min(kVec, e.count * p.G - vb * kVec);
     if (nvec <= 0) return;
     const int v0 = vb * kVec;
-    T* out = (T*)p.out;
+    float* out = (float*)p.out;
     auto out_row = [&](int j) {   // vector j of this block
         const int r = (v0 + j) / p.G, h = (v0 + j) % p.G;
         return out + ((size_t)(e.start + r) * p.nq + (size_t)g * p.G + h) * D;
     };
     if (e.bad) {
         if (split == 0)
-            for (int x = tid; x < nvec * D; x += blockDim.x) stf(out_row(x / D) + x % D, 0.f);
+            for (int x = tid; x < nvec * D; x += blockDim.x) out_row(x / D)[x % D] = 0.f;
         return;
     }
     const int r0 = v0 / p.G, r1 = (v0 + nvec - 1) / p.G + 1;
     const KeySpan span = key_span(e.len, e.count, r0, r1, p.causal, p.window, p.sinks, kTile);
-    const int t_lo = (int)((long long)span.nt * split / p.splits), t_hi = (int)((long long)span.nt * (split + 1) / p.splits);
+    // at least a tile for each warp of a split
+    const int splits = min(p.splits, max(1, span.nt / kWarps));
+    if (split >= splits) return;
+    const int t_lo = (int)((long long)span.nt * split / splits), t_hi = (int)((long long)span.nt * (split + 1) / splits);
     // the positions that exist for any row of the block
     const int hi_all = p.causal ? e.len + r1 : e.len + e.count;
 
     for (int x = tid; x < nvec * (D / 4); x += blockDim.x) {
         const int j = x / (D / 4), c = x % (D / 4) * 4, r = (v0 + j) / p.G, h = (v0 + j) % p.G;
-        float f[4];
-        load4((const T*)p.q + (size_t)(e.start + r) * p.q_stride + ((size_t)g * p.G + h) * D + c, f);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sq[j * D + c + k] = f[k] * p.scale_log2;
+        const float4 f = *reinterpret_cast<const float4*>((const float*)p.q + (size_t)(e.start + r) * p.q_stride +
+                                                          ((size_t)g * p.G + h) * D + c);
+        *reinterpret_cast<float4*>(sq + j * D + c) =
+            make_float4(f.x * p.scale_log2, f.y * p.scale_log2, f.z * p.scale_log2, f.w * p.scale_log2);
     }
     __syncthreads();
 
@@ -92,32 +89,50 @@ __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_simt(const __grid_co
         for (int c = 0; c < C; ++c) acc[j][c] = 0.f;
     }
     float* wk = sk + warp * kTile * (D + 4);
+    float* wv = sv + warp * kTile * D;
     float* wp = sp + warp * kVec * kTile;
-    const T* slab = (const T*)p.slab;
-    for (int t = t_lo + warp; t < t_hi; t += kWarps) {
-        const int k0 = span.tile(t) * kTile, key = k0 + lane;
-        // which of the tile's keys any row sees; the others are neither read nor weighted
-        bool any = false;
-        for (int r = r0; r < r1; ++r)
-            any |= key_visible(key, e.len + r, p.causal ? e.len + r + 1 : hi_all, p.window, p.sinks);
-        const unsigned seen = __ballot_sync(0xffffffffu, any);
-        if (!seen) continue;
-        long long row = 0;    // slab row of this lane's key
-        if (any) {
-            const long long pg = p.table ? p.table[(size_t)e.seq * p.max_pages + (key >> p.ps_log2)] : e.seq;
-            const int in = p.table ? key & ((1 << p.ps_log2) - 1) : key;
-            row = pg * p.rows_page + p.row_layer + (long long)g * p.rows_kv + in;
-        }
-#pragma unroll 4
-        for (int k = 0; k < kTile; ++k) {
-            const long long rk = __shfl_sync(0xffffffffu, row, k);
-            if (!((seen >> k) & 1)) continue;
-            if (lane * 4 < D) {
-                float f[4];
-                load4(slab + rk * D + lane * 4, f);
-                *reinterpret_cast<float4*>(wk + k * (D + 4) + lane * 4) = make_float4(f[0], f[1], f[2], f[3]);
+    const float* slab = (const float*)p.slab;
+    // The warp's next tile from t on in which some row sees a key: its first key, the keys that
+    // any row sees (the others are neither read nor weighted), and this lane's key's slab row.
+    struct Tile { int t, k0; unsigned seen; long long row; };
+    auto find = [&](int t) -> Tile {
+        for (; t < t_hi; t += kWarps) {
+            const int k0 = span.tile(t) * kTile, key = k0 + lane;
+            bool any = false;
+            for (int r = r0; r < r1; ++r)
+                any |= key_visible(key, e.len + r, p.causal ? e.len + r + 1 : hi_all, p.window, p.sinks);
+            const unsigned seen = __ballot_sync(0xffffffffu, any);
+            if (!seen) continue;
+            long long row = 0;
+            if (any) {
+                const long long pg = p.table ? p.table[(size_t)e.seq * p.max_pages + (key >> p.ps_log2)] : e.seq;
+                const int in = p.table ? key & ((1 << p.ps_log2) - 1) : key;
+                row = pg * p.rows_page + p.row_layer + (long long)g * p.rows_kv + in;
             }
+            return {t, k0, seen, row};
         }
+        return {t_hi, 0, 0u, 0};
+    };
+    auto fetch = [&](const Tile& x, float* to, int ld, long long kind) {
+#pragma unroll 8
+        for (int i = 0; i < kTile; i += 128 / D) {
+            const int k = i + lane / (D / 4), c = lane % (D / 4) * 4;
+            const long long rk = __shfl_sync(0xffffffffu, x.row, k) + kind;
+            if ((x.seen >> k) & 1)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                             ::"r"(smem_u32(to + k * ld + c)), "l"((uint64_t)(slab + rk * D + c)) : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    Tile cur = find(t_lo + warp);
+    if (cur.seen) {
+        fetch(cur, wk, D + 4, 0);
+        fetch(cur, wv, D, p.rows_kind);
+    }
+    while (cur.seen) {
+        const int key = cur.k0 + lane;
+        const bool any = (cur.seen >> lane) & 1;
+        asm volatile("cp.async.wait_group 1;" ::: "memory");      // K
         __syncwarp();
         float s[kVec];
 #pragma unroll
@@ -153,17 +168,25 @@ __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_simt(const __grid_co
 #pragma unroll
             for (int c = 0; c < C; ++c) acc[j][c] *= f;
         }
+        const Tile next = find(cur.t + kWarps);
+        __syncwarp();                                             // K and the weights: read, written
+        if (next.seen) {
+            fetch(next, wk, D + 4, 0);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");  // V
+        } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
         __syncwarp();
 #pragma unroll 4
         for (int k = 0; k < kTile; ++k) {
-            const long long rk = __shfl_sync(0xffffffffu, row, k) + p.rows_kind;
-            if (!((seen >> k) & 1)) continue;
+            if (!((cur.seen >> k) & 1)) continue;
             float v[C];
             if constexpr (C == 4) {
-                load4(slab + rk * D + lane * 4, v);
+                const float4 f = *reinterpret_cast<const float4*>(wv + k * D + lane * 4);
+                v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
             } else {
-                v[0] = ldf(slab + rk * D + lane * 2);
-                v[1] = ldf(slab + rk * D + lane * 2 + 1);
+                const float2 f = *reinterpret_cast<const float2*>(wv + k * D + lane * 2);
+                v[0] = f.x; v[1] = f.y;
             }
 #pragma unroll
             for (int j = 0; j < kVec; ++j)
@@ -173,7 +196,9 @@ __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_simt(const __grid_co
                     for (int c = 0; c < C; ++c) acc[j][c] = fmaf(w, v[c], acc[j][c]);
                 }
         }
-        __syncwarp();
+        __syncwarp();                                             // V has been read
+        if (next.seen) fetch(next, wv, D, p.rows_kind);
+        cur = next;
     }
     // join the warps: o over the K staging, [warp][vector][D]
     __syncthreads();
@@ -203,8 +228,8 @@ __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_simt(const __grid_co
             L += f * sml[w * kVec + j].y;
             o += f * sk[(w * kVec + j) * D + x % D];
         }
-        if (p.splits == 1) {
-            stf(out_row(j) + x % D, L == 0.f ? 0.f : o / L);   // a NaN sum stays one
+        if (splits == 1) {
+            out_row(j)[x % D] = L == 0.f ? 0.f : o / L;   // a NaN sum stays one
         } else {
             part[j * (D + 2) + 2 + x % D] = o;
             if (x % D == 0) {
@@ -213,42 +238,67 @@ __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_simt(const __grid_co
             }
         }
     }
-    if (p.splits == 1) return;
-    __threadfence();
+    if (splits == 1) return;
     __syncthreads();
-    if (tid == 0) last = atomicAdd(&p.counters[item], 1) == p.splits - 1;
+    if (tid == 0) last = atom_add_acq_rel(&p.counters[item], 1) == splits - 1;
     __syncthreads();
     if (!last) return;
-    __threadfence();
     const float* all = p.partial + item * p.splits * SLOT;
     for (int x = tid; x < nvec * D; x += blockDim.x) {
         const int j = x / D;
-        float M = -INFINITY;
-        for (int s = 0; s < p.splits; ++s) M = fmaxf(M, __ldcg(all + s * SLOT + j * (D + 2)));
-        const float base = M == -INFINITY ? 0.f : M;
-        float L = 0.f, o = 0.f;
-        for (int s = 0; s < p.splits; ++s) {
-            const float f = exp2f(__ldcg(all + s * SLOT + j * (D + 2)) - base);
-            L += f * __ldcg(all + s * SLOT + j * (D + 2) + 1);
-            o += f * __ldcg(all + s * SLOT + j * (D + 2) + 2 + x % D);
+        const float* q = all + j * (D + 2);
+        float M = -INFINITY, L = 0.f, o = 0.f;
+        for (int s0 = 0; s0 < splits; s0 += 8) {      // eight partials' loads in flight
+            float m8[8], l8[8], o8[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float* z = q + min(s0 + k, splits - 1) * SLOT;
+                m8[k] = __ldcg(z);
+                l8[k] = __ldcg(z + 1);
+                o8[k] = __ldcg(z + 2 + x % D);
+            }
+            float nm = M;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) nm = fmaxf(nm, m8[k]);
+            const float base = nm == -INFINITY ? 0.f : nm, g = exp2f(M - base);
+            M = nm;
+            L *= g;
+            o *= g;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (s0 + k >= splits) break;
+                const float f = exp2f(m8[k] - base);
+                L += f * l8[k];
+                o += f * o8[k];
+            }
         }
-        stf(out_row(j) + x % D, L == 0.f ? 0.f : o / L);
+        out_row(j)[x % D] = L == 0.f ? 0.f : o / L;
     }
     if (tid == 0) p.counters[item] = 0;
 }
 
-template <typename T, int D>
-int launch_simt(PagedAttnParams& p, int num_sms, cudaStream_t st) {
-    const int smem = F32Smem<T>::bytes(D);
-    auto kern = k_paged_attn_simt<T, D>;
-    if (!allow_smem<D * 8 + 7>((const void*)kern, smem)) return 1;
-    const long long vbs = ((long long)p.max_rows * p.G + kVec - 1) / kVec;
+template <int D, int V>
+int launch_dv(PagedAttnParams& p, int num_sms, cudaStream_t st) {
+    constexpr int smem = smem_bytes(D, V);
+    if (!allow_smem<D * 100 + V>((const void*)k_paged_attn_f32<D, V>, smem)) return 1;
+    const long long vbs = ((long long)p.max_rows * p.G + V - 1) / V;
     const long long items = vbs * p.nkv * p.n;
-    // two blocks' worth of items per SM, no item split into less than its tiles
-    p.splits = 1;
-    if (items < 2 * num_sms) p.splits = (int)std::min<long long>(kMaxSplits, 2LL * std::min(num_sms, kPagedCtas) / items);
-    if (p.splits < 1) p.splits = 1;
-    return (int)launch_k(kern, dim3((unsigned)(vbs * p.nkv * p.splits), p.n), dim3(kWarps * 32), smem, st, p);
+    // Two waves of blocks (3 fit on an SM at 64, 1 at 128), so that every SM has work and entries
+    // of different lengths even out: fewer items are split (80 items of 1 to 2235 keys: 118 us
+    // with one wave, 72 with two).
+    const long long target = 2LL * std::min(num_sms, kPagedCtas) * (D == 64 ? 3 : 1);
+    p.splits = (int)std::max(1LL, std::min<long long>(kMaxSplits, target / items));
+    return (int)launch_k(k_paged_attn_f32<D, V>, dim3((unsigned)(vbs * p.nkv * p.splits), p.n), dim3(kWarps * 32), smem,
+                         st, p);
+}
+// 8 vectors a block share K and V; with fewer in all, loops over the missing ones cost as much as
+// the others (2 vectors: 11.7 us with room for 8).
+template <int D>
+int launch_d(PagedAttnParams& p, int num_sms, cudaStream_t st) {
+    const long long vectors = (long long)p.max_rows * p.G;
+    if (vectors <= 2) return launch_dv<D, 2>(p, num_sms, st);
+    if (vectors <= 4) return launch_dv<D, 4>(p, num_sms, st);
+    return launch_dv<D, 8>(p, num_sms, st);
 }
 
 }  // namespace
@@ -259,7 +309,7 @@ size_t paged_scratch_bytes() {
 
 int launch_paged_attn_f32(PagedAttnParams& p, int d, int num_sms, cudaStream_t st) {
     p.launches = 1;
-    return d == 128 ? launch_simt<float, 128>(p, num_sms, st) : launch_simt<float, 64>(p, num_sms, st);
+    return d == 128 ? launch_d<128>(p, num_sms, st) : launch_d<64>(p, num_sms, st);
 }
 int launch_paged_attn_bf16(PagedAttnParams& p, int d, int num_sms, cudaStream_t st) {
     return p.max_rows * p.G <= 16 ? launch_paged_decode(p, d, num_sms, st) : launch_paged_block(p, d, num_sms, st);
