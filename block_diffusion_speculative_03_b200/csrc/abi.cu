@@ -198,7 +198,7 @@ int validate_config(const dflash_config* c) {
 struct dflash_handle {
     dflash_config cfg;
     dflash_weights w;
-    int num_sms;
+    int num_sms, device;
     uint8_t* ws;
     size_t ws_bytes;
     WsLayout L;
@@ -270,6 +270,7 @@ bool df::cache_view(const dflash_cache* c, CacheView& v) {
     v.n_kv_heads = g.n_kv_heads;
     v.head_dim = g.head_dim;
     v.dtype = g.dtype;
+    v.device = c->h->device;
     return true;
 }
 
@@ -562,6 +563,7 @@ int dflash_create(const dflash_config* cfg, const dflash_weights* w, void* works
     h->cfg = c;
     h->w = *w;
     h->num_sms = prop.multiProcessorCount;
+    h->device = dev;
     h->ws = (uint8_t*)workspace;
     h->ws_bytes = ws_bytes;
     h->L = L;
@@ -722,6 +724,7 @@ int dflash_cache_set_window(dflash_cache* c, int window, int sinks, void* scratc
     if (bytes < paged_scratch_bytes()) return DFLASH_WORKSPACE;
     const int d = c->h->cfg.head_dim;
     const uint64_t rows = (uint64_t)c->batch * c->s_req / d;
+    if (rows >= (1ull << 31) || c->batch > kPoolMaxSeqs) return DFLASH_UNSUPPORTED;   // as a pool's
     if (!encode_kv_rows(&c->tm_window, c->slab, rows, d, 64, d / 64) ||
         !encode_kv_rows(&c->tm_window_half, c->slab, rows, d, 64, 1))
         return DFLASH_CUDA;

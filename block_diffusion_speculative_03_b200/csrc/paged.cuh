@@ -55,7 +55,7 @@ struct SlabView {
 // What abi.cu knows of a cache (its struct is private to it).
 struct CacheView {
     SlabView slab;
-    int n_layers, n_kv_heads, head_dim, dtype;
+    int n_layers, n_kv_heads, head_dim, dtype, device;
 };
 bool cache_view(const dflash_cache* c, CacheView& v);
 

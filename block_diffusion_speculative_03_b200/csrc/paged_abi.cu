@@ -82,9 +82,9 @@ int done(dflash_pool* p, int e, int launches) {
     return DFLASH_OK;
 }
 
-// The cache has the pool's layers, heads and type.
+// The cache has the pool's device, layers, heads and type.
 bool same_shape(const dflash_pool* p, const CacheView& c) {
-    return c.n_layers == p->cfg.n_layers && c.n_kv_heads == p->cfg.n_kv_heads && c.head_dim == p->cfg.head_dim &&
+    return c.device == p->device && c.n_layers == p->cfg.n_layers && c.n_kv_heads == p->cfg.n_kv_heads && c.head_dim == p->cfg.head_dim &&
            c.dtype == p->cfg.dtype;
 }
 

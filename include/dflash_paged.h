@@ -22,7 +22,8 @@
  *
  * Conventions (beside those of dflash.h)
  *   - seqs: device int32[n] of sequence ids, or NULL for 0..n-1.  An entry of -1
- *     is padding: nothing is done for it.  n <= max_seqs; n == 0 is a no-op.
+ *     is padding: nothing is done for it.  n <= max_seqs (attention, which may list a
+ *     sequence more than once: n <= 1024); n == 0 is a no-op.
  *   - A sequence that occurs again later in a list of a call that changes
  *     sequences is processed for its first entry only (device error INVALID_ARG);
  *     ids outside [-1, max_seqs) likewise are skipped with INVALID_ARG.
@@ -169,6 +170,9 @@ int dflash_pages_load(dflash_pool* p, const int32_t* seqs, dflash_cache* c, cons
  *   out = R( sum_k P_k v_k / sum_k 2^(t_k - b) ),  P_k = 2^(t_k - b),
  * for an integer b; bf16 pools round P_k to bf16 before it weights v (as
  * dflash_draft_block), fp32 pools do not round it.
+ * The keys of an entry may be split over the device in a way that depends on the
+ * whole call, so a row's result can differ in its last bits when other entries
+ * do; the same call gives the same bits every time.
  * q: device, storage type, row r at q + r * q_stride elements (>= n_q_heads *
  * head_dim, rows 16-byte aligned), a row is [n_q_heads][head_dim].  out: device
  * [total_rows][n_q_heads][head_dim], 16-byte aligned; rows that no entry owns are
@@ -178,7 +182,8 @@ int dflash_pages_load(dflash_pool* p, const int32_t* seqs, dflash_cache* c, cons
  * may hold anything, NaN included; a V row that one query row of an entry sees and
  * another does not must be finite.
  * Device errors: INVALID_ARG (row ranges, row_count > max_rows or negative),
- * CAPACITY (positions without a page). */
+ * CAPACITY (positions without a page), UNSUPPORTED (bf16: 2^31 or more tiles of 64
+ * keys over all rows and heads of the call; nothing is written). */
 int dflash_paged_attention(dflash_pool* p, const int32_t* seqs, int n, int layer, const void* q, int64_t q_stride,
                            const int32_t* row_start, const int32_t* row_count, int total_rows, int max_rows,
                            int causal, int window, int sinks, void* out, dflash_stream stream);
@@ -190,8 +195,10 @@ int dflash_paged_attention(dflash_pool* p, const int32_t* seqs, int n, int layer
  * dflash_ingest_fused_input the causal form of it.  window == 0 turns it off.
  * The cached rows are kept whole, so the window may change between calls.
  * scratch: device memory of dflash_window_scratch_bytes, 256-byte aligned,
- * borrowed until the window is turned off or the cache released, and cleared here
- * on `stream`; one cache uses it at a time. */
+ * borrowed until the window is turned off or the cache released (and while a graph
+ * captured with it may still be replayed), and cleared here on `stream`; one cache
+ * uses it at a time.  DFLASH_UNSUPPORTED: fp32 handles, more than 1024 requests, or
+ * a slab of 2^31 or more rows of one head's K or V. */
 int dflash_window_scratch_bytes(size_t* bytes);
 int dflash_cache_set_window(dflash_cache* c, int window, int sinks, void* scratch, size_t bytes, dflash_stream stream);
 
