@@ -241,14 +241,14 @@ int dflash_pages_write(dflash_pool* p, const int32_t* seqs, int n, int layer, co
     if (layer < 0 || layer >= p->cfg.n_layers || total_rows < 0 || max_rows < 0 || !row_start != !row_count)
         return DFLASH_INVALID_ARG;
     if (!row_start && (max_rows < 1 || total_rows < n)) return DFLASH_INVALID_ARG;
-    if (n == 0 || max_rows == 0) return DFLASH_OK;
+    if (n == 0 || max_rows == 0 || total_rows == 0) return DFLASH_OK;
     const int es = p->cfg.dtype == DFLASH_BF16 ? 2 : 4;
     const int64_t width = (int64_t)p->cfg.n_kv_heads * p->cfg.head_dim;
     if (!aligned16(k) || !aligned16(v) || stride < width || stride > (INT64_MAX >> 4) || (stride * es) % 16)
         return DFLASH_INVALID_ARG;
     if (!row_start) max_rows = 1;
     return done(p, launch_pages_write(p->v, seqs, n, layer, k, v, stride * es, row_start, row_count, total_rows,
-                                      std::min(max_rows, p->cfg.max_len), S(stream)), 1);
+                                      std::min(std::min(max_rows, total_rows), p->cfg.max_len), S(stream)), 1);
 }
 
 int dflash_pages_advance(dflash_pool* p, const int32_t* seqs, const int32_t* row_count, int n, dflash_stream stream) {

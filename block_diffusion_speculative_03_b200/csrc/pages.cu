@@ -292,7 +292,8 @@ __global__ void __launch_bounds__(32) k_pages_copy_whole(PoolView v) {
                        "l"(once)
                      : "memory");
     };
-    for (long long i = 0; i < kBulkStages && i < mine; ++i) load(i);
+    long long loaded = 0;
+    while (loaded < kBulkStages && loaded < mine) load(loaded++);
     for (long long i = 0; i < mine; ++i) {
         const int st = (int)(i % kBulkStages);
         if (!mbar_wait(&full[st], (uint32_t)((i / kBulkStages) & 1), &abort_s, v.status)) break;
@@ -301,16 +302,17 @@ __global__ void __launch_bounds__(32) k_pages_copy_whole(PoolView v) {
         asm volatile("cp.async.bulk.global.shared::cta.bulk_group.L2::cache_hint [%0], [%1], %2, %3;"
                      ::"l"((uint64_t)(v.slab + to)), "r"(smem_u32(ring + st * kBulkChunk)), "r"(n), "l"(once) : "memory");
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        if (i >= 1 && i - 1 + kBulkStages < mine) {
+        if (i >= 1 && loaded < mine) {
             // the stage of the chunk before is free once its store has read it
             asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-            load(i - 1 + kBulkStages);
+            load(loaded++);
         }
     }
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (abort_s) {      // copies in land before the block exits
         volatile int never = 0;
-        for (int k = 0; k < kBulkStages; ++k) mbar_wait(&full[k], 0, &never, nullptr);
+        for (long long k = loaded < kBulkStages ? 0 : loaded - kBulkStages; k < loaded; ++k)
+            mbar_wait(&full[k % kBulkStages], (uint32_t)((k / kBulkStages) & 1), &never, nullptr);
     }
 }
 

@@ -175,7 +175,7 @@ int dflash_pages_load(dflash_pool* p, const int32_t* seqs, dflash_cache* c, cons
  * do; the same call gives the same bits every time.
  * q: device, storage type, row r at q + r * q_stride elements (>= n_q_heads *
  * head_dim, rows 16-byte aligned), a row is [n_q_heads][head_dim].  out: device
- * [total_rows][n_q_heads][head_dim], 16-byte aligned; rows that no entry owns are
+ * [total_rows][n_q_heads][head_dim], 16-byte aligned, no part of q; rows that no entry owns are
  * not written, rows of a skipped entry are zero.  Entries may list the same
  * sequence and must not own the same row.
  * Cached rows past the last position, and rows that no query row of the call sees,
