@@ -496,8 +496,8 @@ __global__ void k_tables_apply(PoolView v, const int* lens, const int* table) {
 }
 
 // The three steps in one block, for tables that it goes through faster than two more launches
-// take (4096 entries: 5 us against 8; 10000: 15).
-constexpr int kSmallTables = 4096;
+// take (1024 entries: 2.7 us against 3.5; 2048: 3.8 both; 8192: 9.5 against 4.0).
+constexpr int kSmallTables = 2048;
 __global__ void __launch_bounds__(kPlan) k_tables_small(PoolView v, const int* lens, const int* table) {
     griddep_wait();
     griddep_launch();
@@ -625,38 +625,87 @@ __global__ void k_exchange_plan(PoolView v, const int* __restrict__ seqs, SlabVi
         else v.recs[i] = make_int4(s, b, from, to);
     }
 }
-// Step 2: a warp copies 16 positions of one (layer, kind, head) run; blocks stride
-// over the entry's units.  (16 divides every page size, so a unit lies in one page.)
-__global__ void __launch_bounds__(256) k_exchange_copy(PoolView v, SlabView c, int load) {
+// Step 2: bound by HBM, every byte read once and written once.  A run of positions of one (layer, kind,
+// head) is contiguous in a page and in the cache, so it moves as bulk copies through shared memory
+// (chunks of at most 16 KB and one page, 2^lp positions), kExStages of them in flight; two
+// one-warp blocks on an SM.  Lanes look the addresses of 32 chunks up together.  (A warp per 4 KB
+// through registers: 5.2 TB/s at 32 contexts of 2048 of 5 layers and 8 heads of 128.)
+constexpr int kExStages = 6, kExChunk = 16384;
+__global__ void __launch_bounds__(32) k_exchange_copy(PoolView v, SlabView c, int load, int lp) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = smem_align_up<uint8_t>(smem_raw, 128);
+    __shared__ uint64_t full[kExStages];
+    __shared__ uint8_t *from_s[64], *to_s[64];
+    __shared__ uint32_t bytes_s[64];
+    __shared__ int abort_s;
     griddep_wait();
     griddep_launch();
     const int4 r = v.recs[blockIdx.y];
     if (r.w <= r.z) return;
-    const int lane = threadIdx.x & 31;
-    const int u0 = r.z >> 4, u1 = (r.w + 15) >> 4;
-    const int runs = v.n_layers * 2 * v.nkv;
-    const long long units = (long long)(u1 - u0) * runs;
-    for (long long u = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); u < units; u += (long long)gridDim.x * 8) {
-        const int run = (int)(u / (u1 - u0)), blk = u0 + (int)(u % (u1 - u0));
-        const int g = run % v.nkv, kind = run / v.nkv % 2, layer = run / v.nkv / 2;
-        const int p0 = max(r.z, blk * 16), p1 = min(r.w, blk * 16 + 16);
-        const int page = v.table[(size_t)r.x * v.max_pages + (p0 >> v.ps_log2)];
-        uint8_t* a = v.slab + (size_t)page * v.page_bytes + (size_t)run * v.ps * v.row_bytes +
-                     (size_t)(p0 & (v.ps - 1)) * v.row_bytes;
-        uint8_t* b = c.slab + (size_t)r.y * c.s_req + (size_t)layer * c.s_layer + (size_t)kind * c.s_kind +
-                     (size_t)g * c.s_kv + (size_t)p0 * v.row_bytes;
-        const uint4* from = reinterpret_cast<const uint4*>(load ? a : b);
-        uint4* to = reinterpret_cast<uint4*>(load ? b : a);
-        const int nv = (p1 - p0) * v.row_bytes >> 4;      // at most 16 * 512 / 16
-        for (int w0 = 0; w0 < nv; w0 += 256) {
-            uint4 x[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (w0 + lane + 32 * k < nv) x[k] = __ldcs(from + w0 + lane + 32 * k);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (w0 + lane + 32 * k < nv) to[w0 + lane + 32 * k] = x[k];
+    const int lane = threadIdx.x;
+    const int u0 = r.z >> lp, nb = ((r.w + (1 << lp) - 1) >> lp) - u0;
+    const long long units = (long long)nb * v.n_layers * 2 * v.nkv;
+    const long long mine = units > blockIdx.x ? (units - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+    if (mine == 0) return;
+    if (lane == 0) {
+        abort_s = 0;
+        for (int i = 0; i < kExStages; ++i) mbar_init(&full[i], 1);
+        fence_mbar_init();
+    }
+    const uint64_t once = make_l2_policy_evict_first();
+    auto issue = [&](long long i) {       // the load of this block's chunk i
+        if ((i & 31) == 0) {
+            if (i + lane < mine) {
+                const long long u = blockIdx.x + (i + lane) * gridDim.x;
+                const int run = (int)(u / nb), blk = u0 + (int)(u % nb);
+                const int g = run % v.nkv, kind = run / v.nkv % 2, layer = run / v.nkv / 2;
+                const int p0 = max(r.z, blk << lp), p1 = min((long long)r.w, (long long)(blk + 1) << lp);
+                const int page = v.table[(size_t)r.x * v.max_pages + (p0 >> v.ps_log2)];
+                uint8_t* a = v.slab + (size_t)page * v.page_bytes + (size_t)run * v.ps * v.row_bytes +
+                             (size_t)(p0 & (v.ps - 1)) * v.row_bytes;
+                uint8_t* b = c.slab + (size_t)r.y * c.s_req + (size_t)layer * c.s_layer + (size_t)kind * c.s_kind +
+                             (size_t)g * c.s_kv + (size_t)p0 * v.row_bytes;
+                const int at = (int)(i + lane) & 63;
+                from_s[at] = load ? a : b;
+                to_s[at] = load ? b : a;
+                bytes_s[at] = (uint32_t)(p1 - p0) * v.row_bytes;
+            }
+            __syncwarp();
         }
+        if (lane == 0) {
+            const int st = (int)(i % kExStages), at = (int)(i & 63);
+            mbar_arrive_expect_tx(&full[st], bytes_s[at]);
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
+                ::"r"(smem_u32(ring + st * kExChunk)), "l"((uint64_t)from_s[at]), "r"(bytes_s[at]),
+                  "r"(smem_u32(&full[st])), "l"(once)
+                : "memory");
+        }
+    };
+    __syncwarp();
+    long long loaded = 0;
+    while (loaded < kExStages && loaded < mine) issue(loaded++);
+    for (long long i = 0; i < mine; ++i) {
+        const int st = (int)(i % kExStages), at = (int)(i & 63);
+        const bool ok = mbar_wait(&full[st], (uint32_t)((i / kExStages) & 1), &abort_s, v.status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (lane == 0) {
+            asm volatile("cp.async.bulk.global.shared::cta.bulk_group.L2::cache_hint [%0], [%1], %2, %3;"
+                         ::"l"((uint64_t)to_s[at]), "r"(smem_u32(ring + st * kExChunk)), "r"(bytes_s[at]), "l"(once)
+                         : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+        if (i >= 1 && loaded < mine) {
+            // the stage of the chunk before is free once its store has read it
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            issue(loaded++);
+        }
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (abort_s && lane == 0) {      // copies in land before the block exits
+        volatile int never = 0;
+        for (long long k = loaded < kExStages ? 0 : loaded - kExStages; k < loaded; ++k)
+            mbar_wait(&full[k % kExStages], (uint32_t)((k / kExStages) & 1), &never, nullptr);
     }
 }
 // Step 3: the lengths.
@@ -715,8 +764,9 @@ int launch_pages_free(const PoolView& v, const int* seqs, const int* keep, int n
 }
 
 int launch_pages_compact(const PoolView& v, int* used, cudaStream_t st, int* launches) {
-    // small tables are followed up by the planning block itself
-    const bool small = (size_t)v.max_seqs * v.max_pages <= kSmallTables;
+    // small tables are followed up by the planning block itself (2048 entries: 5.6 us against 6.0 with
+    // a launch for it; 16384: 11.4 against 11.1)
+    const bool small = (size_t)v.max_seqs * v.max_pages <= 8192;
     *launches = small ? 2 : 3;
     cudaError_t e = launch_k(k_pages_compact, dim3(1), dim3(kPlan), 0, st, v, used, small ? 1 : 0);
     if (e == cudaSuccess && !small)
@@ -739,11 +789,13 @@ int launch_pages_advance(const PoolView& v, const int* seqs, const int* row_coun
 
 int launch_pages_exchange(const PoolView& v, const int* seqs, const SlabView& c, const int* reqs, int n, bool load,
                           cudaStream_t st) {
-    const long long units = (((long long)v.max_len + 15) >> 4) * v.n_layers * 2 * v.nkv;
-    const long long want = (units + 7) / 8, cap = (148 * 8 + n - 1) / n;
-    const int bx = (int)(want < cap ? want : cap);
+    constexpr int smem = kExStages * kExChunk + 128;
+    if (!allow_smem<2>((const void*)k_exchange_copy, smem)) return 1;
+    int lp = v.ps_log2;
+    while (v.row_bytes << lp > kExChunk) --lp;
+    const int bx = (2 * 148 + n - 1) / n;
     cudaError_t e = launch_k(k_exchange_plan, dim3(n), dim3(256), 0, st, v, seqs, c, reqs, load ? 1 : 0);
-    if (e == cudaSuccess) e = launch_k(k_exchange_copy, dim3(bx, n), dim3(256), 0, st, v, c, load ? 1 : 0);
+    if (e == cudaSuccess) e = launch_k(k_exchange_copy, dim3(bx, n), dim3(32), smem, st, v, c, load ? 1 : 0, lp);
     if (e == cudaSuccess) e = launch_k(k_exchange_end, dim3(1), dim3(kPlan), 0, st, v, c, n, load ? 1 : 0);
     return (int)e;
 }
