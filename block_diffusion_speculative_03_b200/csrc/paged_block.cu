@@ -14,7 +14,8 @@
 //              bf16(2^(t - b)), rescale O by an exact power of two when b moves.
 //   warp 0, 11 TMA: K and V tiles of 64 keys, one box per page and 64-column half; warp 0 also
 //              stages the next stretch's Q.
-//   warp 1     tcgen05.mma: S = Q K^T of a group's next tile once it has read the one before.
+//   warp 1     tcgen05.mma: S = Q K^T into the next of three buffers; a tile's P takes the place of
+//              its S, so a buffer is free again when the tile's product is done.
 //   warp 10    tcgen05.mma: O += P V once P is there.  (Two issuers that each wait for one thing:
 //              one that polled for both took 300 to 700 cycles to notice either.)
 //
@@ -47,8 +48,8 @@ template <int D> struct BlockCfg {
     static constexpr int SMEM = 1024 + RING + JOIN + 2 * 128 * 8 + 128 * QLD + kLineBytes + 512;
     static_assert(SMEM <= 227 * 1024, "shared memory");
     static constexpr int SLOT = 128 * (D + 2);               // floats of a partial
-    // tensor memory columns: S[2] (64 each), P[2] (32 bf16 pairs each), Q (D / 2), O[2] (D each)
-    static constexpr uint32_t T_S = 0, T_P = 128, T_Q = 192, T_O = 256, COLS = 512;
+    // tensor memory columns: S[3] (64 each; P over the first 32), Q (D / 2), O[2] (D each)
+    static constexpr uint32_t T_S = 0, T_Q = 192, T_O = 256, COLS = 512;
 };
 
 // The lowest n bits (n below 0: none, above 32: all).
@@ -90,11 +91,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
     uint8_t* line_mem = q_stage + 128 * C::QLD;
     uint64_t* kv_full = (uint64_t*)(line_mem + kLineBytes);          // [2][S]: K, V
     uint64_t* kv_empty = kv_full + 2 * S;                            // [2][S]
-    uint64_t* s_full = kv_empty + 2 * S;                             // [2]
-    uint64_t* p_full = s_full + 2;                                   // [2]
-    uint64_t* o_done = p_full + 2;                                   // [2]
-    uint64_t* s_read = o_done + 2;                                   // [2]
-    uint64_t* q_full = s_read + 2;
+    uint64_t* s_full = kv_empty + 2 * S;                             // [3]: by buffer, as the next two
+    uint64_t* p_full = s_full + 3;                                   // [3]
+    uint64_t* pv_done = p_full + 3;                                  // [3]
+    uint64_t* q_full = pv_done + 3;
     uint64_t* q_free = q_full + 1;
     uint64_t* q_staged = q_free + 1;
     uint64_t* drain = q_staged + 1;                                  // [2]
@@ -109,13 +109,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             mbar_init(&kv_full[i], 1);
             mbar_init(&kv_empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 3; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&s_read[i], 4);
             mbar_init(&p_full[i], 4);
-            mbar_init(&o_done[i], 1);
-            mbar_init(&drain[i], 1);
+            mbar_init(&pv_done[i], 1);
         }
+        mbar_init(&drain[0], 1);
+        mbar_init(&drain[1], 1);
         mbar_init(q_full, 4);
         mbar_init(q_free, 8);
         mbar_init(q_staged, 64);
@@ -145,19 +145,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
         tc_fence_after();
         tmem = *tmem_slot;
     }
-    const uint32_t tS = tmem + C::T_S, tP = tmem + C::T_P, tQ = tmem + C::T_Q, tO = tmem + C::T_O;
+    const uint32_t tS = tmem + C::T_S, tQ = tmem + C::T_Q, tO = tmem + C::T_O;
 
     if (warp == 0 || warp > kPvWarp) {
         // ------------------------------------------------------------ TMA producers, K and V
         // Rings of their own: a K tile is free again as soon as its S is done, a V tile when its
-        // product is (one ring for both held every stage for the softmax's time too: 4 stages
-        // then cost 1090 cycles a tile, whatever the softmax did).
+        // product is.  Lanes look up the boxes of the next tiles together, one box (both halves)
+        // each: what is left to do between a free stage and its load is a few instructions.  (Looked
+        // up tile by tile that took 700 cycles, which three stages do not hide.)
         const int kind = warp == 0 ? 0 : 1;
         uint64_t *full = kv_full + kind * S, *empty = kv_empty + kind * S;
         uint8_t* tiles = ring + kind * S * C::KV;
         const int bl = p.table ? min(p.ps_log2, 6) : 6;          // log2 rows of a box
         const int box_rows = 1 << bl, boxes = 64 >> bl;
-        const int b = lane & (boxes - 1), h = lane / boxes;       // this lane's box and 64-column half
+        const int batch = 32 >> (6 - bl);                         // tiles looked up at a time: 32 boxes
+        const int b = lane & (boxes - 1), tile_of = lane >> (6 - bl);   // this lane's box and tile of a batch
+        const uint32_t tile_boxes = (1u << boxes) - 1u;
         Stretch nx;
         bool more = walk.next(line, nx);
         int it = 0;
@@ -175,30 +178,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             const int4 e = line.ent[s.i];
             const int hi = p.causal ? e.w + s.r1 : e.w + e.z;
             const int lo = p.window > 0 ? max(0, e.w + s.r0 - p.window + 1) : 0;
-            PageLookup look;
-            look.reset();
+            int row = -1;                                 // slab row of the lane's box, -1: not loaded
+            uint32_t wanted = 0;
             for (int t = s.t0; t < s.t1; ++t, ++it) {
-                const int k0 = s.span.tile(t) * 64, st = it % S, kb = k0 + b * box_rows;
-                const int page = look.at(p, e.x, k0, kb, boxes, lane);
-                const bool want = h < C::HALVES && kb < hi && (kb < p.sinks || kb + box_rows > lo) && page >= 0;
+                const int j = (t - s.t0) & (batch - 1), st = it % S;
+                if (j == 0) {
+                    row = -1;
+                    const int kb = s.span.tile(t + tile_of) * 64 + b * box_rows;
+                    if (t + tile_of < s.t1 && kb < hi && (kb < p.sinks || kb + box_rows > lo)) {
+                        const int page = p.table ? p.table[(size_t)e.x * p.max_pages + (kb >> p.ps_log2)] : e.x;
+                        if (page >= 0)
+                            row = (int)((long long)page * p.rows_page + p.row_layer + (long long)s.g * p.rows_kv +
+                                        kind * p.rows_kind + (p.table ? kb & ((1 << p.ps_log2) - 1) : kb));
+                    }
+                    wanted = __ballot_sync(0xffffffffu, row >= 0);
+                }
+                const int n_want = __popc((wanted >> (j * boxes)) & tile_boxes);
                 ok = mbar_wait_short(&empty[st], (uint32_t)(((it / S) & 1) ^ 1), abort_flag, p.wait_status);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
                 }
-                const int n_want = __popc(__ballot_sync(0xffffffffu, want));
-                if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(n_want * box_rows * 128));
-                __syncwarp();
-                if (want) {
-                    const long long row = (long long)page * p.rows_page + p.row_layer + (long long)s.g * p.rows_kv +
-                                          kind * p.rows_kind + (p.table ? kb & ((1 << p.ps_log2) - 1) : kb);
-                    asm volatile(
-                        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
-                        "[%0], [%1, {%2, %3, %4}], [%5];"
-                        ::"r"(smem_u32(tiles + st * C::KV + h * 8192 + b * box_rows * 128)), "l"((uint64_t)&p.tmap_half),
-                          "r"(0), "r"((int)row), "r"(h), "r"(smem_u32(&full[st]))
-                        : "memory");
+                if (tile_of == j) {
+                    if (b == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(n_want * box_rows * 128 * C::HALVES));
+                    if (row >= 0) {
+#pragma unroll
+                        for (int h = 0; h < C::HALVES; ++h)
+                            asm volatile(
+                                "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
+                                "[%0], [%1, {%2, %3, %4}], [%5];"
+                                ::"r"(smem_u32(tiles + st * C::KV + h * 8192 + b * box_rows * 128)),
+                                  "l"((uint64_t)&p.tmap_half), "r"(0), "r"(row), "r"(h), "r"(smem_u32(&full[st]))
+                                : "memory");
+                    }
                 }
+                __syncwarp();
                 // (with S tiles issued since, the first tile's S is done, and so Q was taken)
                 if (t - s.t0 >= S && staged < 128) stage_some(staged + 16);
             }
@@ -219,8 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
         // ------------------------------------------------------------ S = Q K^T
         // The whole warp walks and waits, one elected lane issues: in code that the warp runs
         // together the operands stay in uniform registers (128 x 64 x 16 measured 33 cycles an
-        // instruction against 47-70 in a branch of one lane).  S of tile j + 2 goes where S of
-        // tile j was, as soon as the softmax has read that, so a group finds its next S waiting.
+        // instruction against 47-70 in a branch of one lane).
         constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 64);
         const bool leader = elect_one();
         int it = 0, seg = 0;
@@ -230,17 +243,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             for (int t = s.t0; t < s.t1 && ok; ++t, ++it) {
                 const int st = it % S;
                 ok = mbar_wait_short(&kv_full[st], (uint32_t)((it / S) & 1), abort_flag, p.wait_status);
-                if (ok && it >= 2) ok = mbar_wait_short(&s_read[it & 1], (uint32_t)(((it - 2) >> 1) & 1), abort_flag, p.wait_status);
+                if (ok && it >= 3) ok = mbar_wait_short(&pv_done[it % 3], (uint32_t)((it / 3 - 1) & 1), abort_flag, p.wait_status);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t ka = smem_u32(ring + st * C::KV), d = tS + (it & 1) * 64;
+                const uint32_t ka = smem_u32(ring + st * C::KV), d = tS + (it % 3) * 64;
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
                         tc_mma_bf16_ts(d, tQ + kk * 8, umma_desc_sw128(ka + (kk >> 2) * 8192) + 2 * (kk & 3), IDESC_S,
                                        kk > 0 ? 1u : 0u);
-                    tc_commit(&s_full[it & 1]);
+                    tc_commit(&s_full[it % 3]);
                     tc_commit(&kv_empty[st]);
                 }
                 __syncwarp();
@@ -260,20 +273,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
         bool ok = true;
         while (ok && walk.next(line, s)) {
             for (int t = s.t0; t < s.t1; ++t, ++it) {
-                const int pb = it & 1;
+                const int sb = it % 3;
                 ok = mbar_wait_short(&kv_full[S + it % S], (uint32_t)((it / S) & 1), abort_flag, p.wait_status);
-                if (ok) ok = mbar_wait_short(&p_full[pb], (uint32_t)((it >> 1) & 1), abort_flag, p.wait_status);
+                if (ok) ok = mbar_wait_short(&p_full[sb], (uint32_t)((it / 3) & 1), abort_flag, p.wait_status);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t va = smem_u32(ring + (S + it % S) * C::KV), d = tO + pb * 128, a = tP + pb * 32;
+                const uint32_t va = smem_u32(ring + (S + it % S) * C::KV), d = tO + (it & 1) * 128, a = tS + sb * 64;
                 const uint32_t add = t >= s.t0 + 2 ? 1u : 0u;
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         tc_mma_bf16_ts(d, a + kk * 8, umma_desc_sw128_mn(va + kk * 2048, 8192, 1024), IDESC_PV,
                                        kk > 0 ? 1u : add);
-                    tc_commit(&o_done[pb]);
+                    tc_commit(&pv_done[sb]);
                     tc_commit(&kv_empty[S + it % S]);
                 }
                 __syncwarp();
@@ -291,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
         const int row = rl % RW, cs = rl / RW, col = cs * KC;  // vector of the tile, first column (warp-uniform)
         const int e256 = tid - 64;
         const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
-        const uint32_t my_s = tS + lanes + w * 64, my_p = tP + lanes + w * 32, my_o = tO + lanes + w * 128;
+        const uint32_t my_o = tO + lanes + w * 128;
         // the lane's vector of stretch n (staged by the producer) into the Q operand; lanes past the
         // tile's vectors take whatever stands there (their rows are not written)
         auto put_q = [&](int n) -> bool {
@@ -321,12 +334,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
         };
         Stretch nx;
         bool more = walk.next(line, nx);
-        if constexpr (CS > 1) {           // the other slices' columns of this lane's P stay zero
-            const uint32_t z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-            for (int c0 = 0; c0 < 32; c0 += 8) tmem_st8u(my_p + c0, z);
-            tmem_wait_st();
-        }
         int it0 = 0, seg = 0;             // tiles and stretches before this one
         bool ok = true;
         if (more) {                       // the first stretch's Q: staged by all softmax threads
@@ -351,21 +358,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             for (int t = s.t0 + ((it0 ^ w) & 1); ok && t < s.t1; t += 2) {
                 const int it = it0 + t - s.t0;
                 last = it;
-                ok = mbar_wait_short(&s_full[w], (uint32_t)((it >> 1) & 1), abort_flag, p.wait_status);
+                const int sb = it % 3;
+                const uint32_t my_s = tS + lanes + sb * 64;            // S, then P
+                ok = mbar_wait_short(&s_full[sb], (uint32_t)((it / 3) & 1), abort_flag, p.wait_status);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                // the product of the group's tile before has read P and written O (looked at early,
-                // waited for where it matters)
-                const bool o_ready = it < 2 || mbar_test(&o_done[w], (uint32_t)(((it - 2) >> 1) & 1));
                 const int k0 = s.span.tile(t) * 64, kvb = k0 + col;
                 float x[KC];
                 if constexpr (KC == 64) tmem_ld64w(my_s, x);
                 else if constexpr (KC == 32) tmem_ld32w(my_s + col, x);
                 else tmem_ld16w(my_s + col, x);
-                tc_fence_before();
-                __syncwarp();
-                mbar_arrive_if(lane == 0, &s_read[w]);
                 // tiles with keys that some row does not see
                 if (k0 + 64 > hi_all || (k0 < lo_all && k0 + 64 > p.sinks)) {
                     // this thread's keys as bits: below the row's end, and from its window on or a sink
@@ -398,14 +401,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                 for (int i = 12; i + 1 < KC; i += 2) m4[(i >> 1) & 3] = fmax3(m4[(i >> 1) & 3], x[i], x[i + 1]);
                 const float nb = floorf(fmax3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * p.scale_log2);
                 const bool grow = nb > base + kBaseLag;
-                if (!__all_sync(0xffffffffu, o_ready)) {
-                    ok = mbar_wait_short(&o_done[w], (uint32_t)(((it - 2) >> 1) & 1), abort_flag, p.wait_status);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                }
-                tc_fence_after();
                 if (__any_sync(0xffffffffu, grow)) {
-                    if (t >= s.t0 + 2) {   // O holds earlier tiles
+                    if (t >= s.t0 + 2) {   // O holds earlier tiles: once the group's product before is done
+                        ok = mbar_wait_short(&pv_done[(it - 2) % 3], (uint32_t)(((it - 2) / 3) & 1), abort_flag, p.wait_status);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        tc_fence_after();
                         const float f = grow ? pow2_int(base - nb - kBaseLead) : 1.0f;
 #pragma unroll 1
                         for (int c0 = 0; c0 < D; c0 += 32) {
@@ -434,14 +435,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                         sum2[(i >> 1) & 1] = add_x2(sum2[(i >> 1) & 1], e2);
                         pk[i / 2] = pack_bf16(e2.x, e2.y);
                     }
-                    tmem_st8u(my_p + col / 2 + c0 / 2, pk);
+                    tmem_st8u(my_s + col / 2 + c0 / 2, pk);
+                }
+                if constexpr (CS > 1) {           // the other slices' columns of this lane's P are zero
+                    const uint32_t z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+                    for (int c0 = 0; c0 < 32; c0 += 8)
+                        if (c0 < col / 2 || c0 >= (col + KC) / 2) tmem_st8u(my_s + c0, z);
                 }
                 sum2[0] = add_x2(sum2[0], sum2[1]);
                 l += sum2[0].x + sum2[0].y;
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                mbar_arrive_if(lane == 0, &p_full[w]);
+                mbar_arrive_if(lane == 0, &p_full[sb]);
             }
             // this warp has read its last S of the stretch; when all have, Q may change
             __syncwarp();
@@ -454,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             }
             ++seg;
             if (ok && last >= 0)
-                ok = mbar_wait_short(&o_done[w], (uint32_t)((last >> 1) & 1), abort_flag, p.wait_status);
+                ok = mbar_wait_short(&pv_done[last % 3], (uint32_t)((last / 3) & 1), abort_flag, p.wait_status);
             ml[w * 128 + rl] = make_float2(base, l);
             if (named_bar_or(1, kSoftmax, !ok)) break;
             tc_fence_after();
