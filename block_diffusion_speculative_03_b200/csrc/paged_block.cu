@@ -36,20 +36,22 @@ constexpr int kThreads = 384;
 constexpr int kSoftmax = 256;    // threads of the two softmax groups
 constexpr int kPvWarp = 10;
 
-template <int D> struct BlockCfg {
+constexpr int kBufs = 5;         // buffers of S in tensor memory
+
+template <int D> constexpr int kSlot = 128 * (D + 2);        // floats of a partial
+
+template <int D, int CS> struct BlockCfg {
     static constexpr int HALVES = D / 64;
     static constexpr int KV = HALVES * 64 * 128;             // bytes of a K (or V) tile
-    static constexpr int STAGES = D == 128 ? 3 : 6;          // of K and of V
+    static constexpr int STAGES = D == 64 ? 6 : CS == 1 ? 4 : 3;   // of K and of V
     static constexpr int RING = STAGES * 2 * KV;
     static constexpr int OLD = D + 4;
-    static constexpr int HLD = D / 2 + 4;
-    static constexpr int JOIN = 256 * HLD * 4;               // >= 128 * OLD * 4
-    static constexpr int QLD = D * 2 + 16;                   // bytes of a staged Q vector: 16 more, so that lanes hit all banks
-    static constexpr int SMEM = 1024 + RING + JOIN + 2 * 128 * 8 + 128 * QLD + kLineBytes + 512;
+    static constexpr int QLD = D * 2 + 16;                   // bytes of a staged vector: 16 more, so that lanes hit all banks
+    static constexpr int JOIN = CS == 1 ? 128 * QLD : 128 * OLD * 4;
+    static constexpr int SMEM = 1024 + RING + JOIN + 4 * 128 * 8 + 128 * QLD + kLineBytes + 512;
     static_assert(SMEM <= 227 * 1024, "shared memory");
-    static constexpr int SLOT = 128 * (D + 2);               // floats of a partial
-    // tensor memory columns: S[3] (64 each; P over the first 32), Q (D / 2), O[2] (D each)
-    static constexpr uint32_t T_S = 0, T_Q = 192, T_O = 256, COLS = 512;
+    // tensor memory columns: S[kBufs] (64 each; P over the first 32), Q (D / 2), O (D)
+    static constexpr uint32_t T_S = 0, T_Q = kBufs * 64, T_O = 384, COLS = 512;
 };
 
 // The lowest n bits (n below 0: none, above 32: all).
@@ -74,27 +76,29 @@ DF_DEV void stage_q(const PagedAttnParams& p, const Line& line, const Stretch& s
         const __nv_bfloat16* src = (const __nv_bfloat16*)p.q + (size_t)(e.y + s.r0 + r) * p.q_stride +
                                    (s.g * p.G + v - r * p.G) * D + c;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
-                     ::"r"(smem_u32(q_stage) + v * BlockCfg<D>::QLD + c * 2), "l"((uint64_t)src) : "memory");
+                     ::"r"(smem_u32(q_stage) + v * BlockCfg<D, 1>::QLD + c * 2), "l"((uint64_t)src) : "memory");
     }
 }
 
 template <int D, int CS>
 __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_constant__ PagedAttnParams p) {
-    using C = BlockCfg<D>;
+    using C = BlockCfg<D, CS>;
     constexpr int S = C::STAGES;
     constexpr int RW = 128 / CS, KC = 64 / CS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = smem_align_up<uint8_t>(smem_raw, 1024);          // K [S], V [S]
-    float* join = (float*)(ring + C::RING);                          // [128][OLD]
-    float2* ml = (float2*)(ring + C::RING + C::JOIN);                // [2][128] base and sum per group and lane
-    uint8_t* q_stage = (uint8_t*)(ml + 256);                         // [128][QLD] the next stretch's Q
+    uint8_t* join = ring + C::RING;                                  // the stretch's rows on their way out
+    float2* ml = (float2*)(join + C::JOIN);                          // [2][128] base and sum per group and lane
+    float* base_s = (float*)(ml + 256);                              // [2][128] the base after a group's tile
+    uint8_t* q_stage = (uint8_t*)(ml + 512);                         // [128][QLD] the next stretch's Q
     uint8_t* line_mem = q_stage + 128 * C::QLD;
     uint64_t* kv_full = (uint64_t*)(line_mem + kLineBytes);          // [2][S]: K, V
     uint64_t* kv_empty = kv_full + 2 * S;                            // [2][S]
-    uint64_t* s_full = kv_empty + 2 * S;                             // [3]: by buffer, as the next two
-    uint64_t* p_full = s_full + 3;                                   // [3]
-    uint64_t* pv_done = p_full + 3;                                  // [3]
-    uint64_t* q_full = pv_done + 3;
+    uint64_t* s_full = kv_empty + 2 * S;                             // [kBufs], as the next two
+    uint64_t* p_full = s_full + kBufs;
+    uint64_t* pv_done = p_full + kBufs;
+    uint64_t* base_set = pv_done + kBufs;                            // [2]
+    uint64_t* q_full = base_set + 2;
     uint64_t* q_free = q_full + 1;
     uint64_t* q_staged = q_free + 1;
     uint64_t* drain = q_staged + 1;                                  // [2]
@@ -109,13 +113,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             mbar_init(&kv_full[i], 1);
             mbar_init(&kv_empty[i], 1);
         }
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < kBufs; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
             mbar_init(&pv_done[i], 1);
         }
-        mbar_init(&drain[0], 1);
-        mbar_init(&drain[1], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&base_set[i], 4);
+            mbar_init(&drain[i], 1);
+        }
         mbar_init(q_full, 4);
         mbar_init(q_free, 8);
         mbar_init(q_staged, 64);
@@ -243,17 +249,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             for (int t = s.t0; t < s.t1 && ok; ++t, ++it) {
                 const int st = it % S;
                 ok = mbar_wait_short(&kv_full[st], (uint32_t)((it / S) & 1), abort_flag, p.wait_status);
-                if (ok && it >= 3) ok = mbar_wait_short(&pv_done[it % 3], (uint32_t)((it / 3 - 1) & 1), abort_flag, p.wait_status);
+                if (ok && it >= kBufs)
+                    ok = mbar_wait_short(&pv_done[it % kBufs], (uint32_t)((it / kBufs - 1) & 1), abort_flag, p.wait_status);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t ka = smem_u32(ring + st * C::KV), d = tS + (it % 3) * 64;
+                const uint32_t ka = smem_u32(ring + st * C::KV), d = tS + (it % kBufs) * 64;
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
                         tc_mma_bf16_ts(d, tQ + kk * 8, umma_desc_sw128(ka + (kk >> 2) * 8192) + 2 * (kk & 3), IDESC_S,
                                        kk > 0 ? 1u : 0u);
-                    tc_commit(&s_full[it % 3]);
+                    tc_commit(&s_full[it % kBufs]);
                     tc_commit(&kv_empty[st]);
                 }
                 __syncwarp();
@@ -273,18 +280,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
         bool ok = true;
         while (ok && walk.next(line, s)) {
             for (int t = s.t0; t < s.t1; ++t, ++it) {
-                const int sb = it % 3;
+                const int sb = it % kBufs;
                 ok = mbar_wait_short(&kv_full[S + it % S], (uint32_t)((it / S) & 1), abort_flag, p.wait_status);
-                if (ok) ok = mbar_wait_short(&p_full[sb], (uint32_t)((it / 3) & 1), abort_flag, p.wait_status);
+                if (ok) ok = mbar_wait_short(&p_full[sb], (uint32_t)((it / kBufs) & 1), abort_flag, p.wait_status);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t va = smem_u32(ring + (S + it % S) * C::KV), d = tO + (it & 1) * 128, a = tS + sb * 64;
-                const uint32_t add = t >= s.t0 + 2 ? 1u : 0u;
+                const uint32_t va = smem_u32(ring + (S + it % S) * C::KV), a = tS + sb * 64;
+                const uint32_t add = t > s.t0 ? 1u : 0u;
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        tc_mma_bf16_ts(d, a + kk * 8, umma_desc_sw128_mn(va + kk * 2048, 8192, 1024), IDESC_PV,
+                        tc_mma_bf16_ts(tO, a + kk * 8, umma_desc_sw128_mn(va + kk * 2048, 8192, 1024), IDESC_PV,
                                        kk > 0 ? 1u : add);
                     tc_commit(&pv_done[sb]);
                     tc_commit(&kv_empty[S + it % S]);
@@ -304,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
         const int row = rl % RW, cs = rl / RW, col = cs * KC;  // vector of the tile, first column (warp-uniform)
         const int e256 = tid - 64;
         const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
-        const uint32_t my_o = tO + lanes + w * 128;
+        const uint32_t my_o = tO + lanes;
         // the lane's vector of stretch n (staged by the producer) into the Q operand; lanes past the
         // tile's vectors take whatever stands there (their rows are not written)
         auto put_q = [&](int n) -> bool {
@@ -354,13 +361,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             const int hi_row = p.causal ? min(pos + 1, hi_tile) : hi_tile;
             const int lo_row = p.window > 0 ? pos - p.window + 1 : 0;
             float base = -INFINITY, l = 0.f;
-            int last = -1;                                             // this group's last tile
             for (int t = s.t0 + ((it0 ^ w) & 1); ok && t < s.t1; t += 2) {
                 const int it = it0 + t - s.t0;
-                last = it;
-                const int sb = it % 3;
+                const int sb = it % kBufs;
                 const uint32_t my_s = tS + lanes + sb * 64;            // S, then P
-                ok = mbar_wait_short(&s_full[sb], (uint32_t)((it / 3) & 1), abort_flag, p.wait_status);
+                ok = mbar_wait_short(&s_full[sb], (uint32_t)((it / kBufs) & 1), abort_flag, p.wait_status);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -400,26 +405,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
 #pragma unroll
                 for (int i = 12; i + 1 < KC; i += 2) m4[(i >> 1) & 3] = fmax3(m4[(i >> 1) & 3], x[i], x[i + 1]);
                 const float nb = floorf(fmax3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * p.scale_log2);
-                const bool grow = nb > base + kBaseLag;
-                if (__any_sync(0xffffffffu, grow)) {
-                    if (t >= s.t0 + 2) {   // O holds earlier tiles: once the group's product before is done
-                        ok = mbar_wait_short(&pv_done[(it - 2) % 3], (uint32_t)(((it - 2) / 3) & 1), abort_flag, p.wait_status);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const float f = grow ? pow2_int(base - nb - kBaseLead) : 1.0f;
-#pragma unroll 1
-                        for (int c0 = 0; c0 < D; c0 += 32) {
-                            float v[32];
-                            tmem_ld32w(my_o + c0, v);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] *= f;
-                            tmem_st16(my_o + c0, v);
-                            tmem_st16(my_o + c0 + 16, v + 16);
-                        }
-                        l *= f;
+                // the base that the tile before left (the other group's, half a turn ago), and this tile's
+                if (t > s.t0) {
+                    ok = mbar_wait_short(&base_set[w ^ 1], (uint32_t)(((it - 1) >> 1) & 1), abort_flag, p.wait_status);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const float before = base_s[(w ^ 1) * 128 + rl];
+                    if (before != base) {
+                        l = base == -INFINITY ? 0.f : l * pow2_int(base - before);
+                        base = before;
                     }
-                    if (grow) base = nb + kBaseLead;
+                }
+                const bool grow = nb > base + kBaseLag;
+                const float held = base;
+                if (grow) base = nb + kBaseLead;
+                base_s[w * 128 + rl] = base;
+                __syncwarp();
+                mbar_arrive_if(lane == 0, &base_set[w]);
+                if (__any_sync(0xffffffffu, grow) && t > s.t0) {
+                    // O holds the tiles before: once their products are done
+                    ok = mbar_wait_short(&pv_done[(it - 1) % kBufs], (uint32_t)(((it - 1) / kBufs) & 1), abort_flag,
+                                         p.wait_status);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const float f = grow ? pow2_int(held - base) : 1.0f;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        float v[32];
+                        tmem_ld32w(my_o + c0, v);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] *= f;
+                        tmem_st16(my_o + c0, v);
+                        tmem_st16(my_o + c0 + 16, v + 16);
+                    }
+                    l *= f;
                 }
                 const float bb = (base == -INFINITY) ? 0.f : base;
                 // two at a time where the hardware has it: instructions are what this loop runs out of
@@ -460,57 +480,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                 if (ok) ok = put_q(seg + 1);
             }
             ++seg;
-            if (ok && last >= 0)
-                ok = mbar_wait_short(&pv_done[last % 3], (uint32_t)((last / 3) & 1), abort_flag, p.wait_status);
+            {
+                const int last = it0 + s.t1 - s.t0 - 1;
+                if (ok) ok = mbar_wait_short(&pv_done[last % kBufs], (uint32_t)((last / kBufs) & 1), abort_flag, p.wait_status);
+            }
             ml[w * 128 + rl] = make_float2(base, l);
             if (named_bar_or(1, kSoftmax, !ok)) break;
             tc_fence_after();
-            // ---- the stretch's rows: the groups' O are added, then the copies of a vector.  Bases
-            // differ by integers, so all factors are exact powers of two.
+            // ---- the stretch's rows: O is relative to the last tile's base; bases differ by integers,
+            // so all factors are exact powers of two.  Each group has half of the columns.
             const bool whole = s.whole(), head = s.t0 == 0;   // head: holds the item's first tile
-            float* slot = p.partial + (size_t)(2 * blockIdx.x + (head ? 1 : 0)) * C::SLOT;
+            float* slot = p.partial + (size_t)(2 * blockIdx.x + (head ? 1 : 0)) * kSlot<D>;
+            constexpr int HC = D / 2;
+            const float B = base_s[((it0 + s.t1 - s.t0 - 1) & 1) * 128 + rl], z = B == -INFINITY ? 0.f : B;
+            const float2 m0 = ml[rl], m1 = ml[128 + rl];
+            const float L = pow2_int(m0.x - z) * m0.y + pow2_int(m1.x - z) * m1.y;
             if constexpr (CS == 1) {
-                // each group finishes half the columns: it gives the other half away
-                constexpr int HC = D / 2;
-                const float2 m0 = ml[rl], m1 = ml[128 + rl];
-                const float B = fmaxf(m0.x, m1.x), z = B == -INFINITY ? 0.f : B;
-                const float g0 = pow2_int(m0.x - z), g1 = pow2_int(m1.x - z), f0 = w ? g1 : g0;
-                const float L = g0 * m0.y + g1 * m1.y, inv = L == 0.f ? 0.f : 1.0f / L;
-                float* mine = join + (w * 128 + rl) * C::HLD;
-                float* theirs = join + ((w ^ 1) * 128 + rl) * C::HLD;
+                const float inv = L == 0.f ? 0.f : 1.0f / L;
 #pragma unroll 1
-                for (int c0 = 0; c0 < HC; c0 += 32) {
+                for (int c0 = w * HC; c0 < (w + 1) * HC; c0 += 32) {
                     float v[32];
-                    tmem_ld32w(my_o + (w ^ 1) * HC + c0, v);
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        *reinterpret_cast<float4*>(mine + c0 + i) =
-                            last >= 0 ? make_float4(f0 * v[i], f0 * v[i + 1], f0 * v[i + 2], f0 * v[i + 3])
-                                      : make_float4(0.f, 0.f, 0.f, 0.f);
-                }
-                named_bar_sync(1, kSoftmax);
-#pragma unroll 1
-                for (int c0 = 0; c0 < HC; c0 += 32) {
-                    float v[32];
-                    tmem_ld32w(my_o + w * HC + c0, v);
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 o = *reinterpret_cast<const float4*>(theirs + c0 + i);
-                        v[i] = (last >= 0 ? f0 * v[i] : 0.f) + o.x;
-                        v[i + 1] = (last >= 0 ? f0 * v[i + 1] : 0.f) + o.y;
-                        v[i + 2] = (last >= 0 ? f0 * v[i + 2] : 0.f) + o.z;
-                        v[i + 3] = (last >= 0 ? f0 * v[i + 3] : 0.f) + o.w;
-                    }
-                    if (whole) {      // as bf16 over what was just read; written out below
+                    tmem_ld32w(my_o + c0, v);
+                    if (whole) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 8)
-                            *reinterpret_cast<uint4*>((uint8_t*)(theirs + c0) + i * 2) =
+                            *reinterpret_cast<uint4*>(join + rl * C::QLD + (c0 + i) * 2) =
                                 make_uint4(pack_bf16(v[i] * inv, v[i + 1] * inv), pack_bf16(v[i + 2] * inv, v[i + 3] * inv),
                                            pack_bf16(v[i + 4] * inv, v[i + 5] * inv), pack_bf16(v[i + 6] * inv, v[i + 7] * inv));
                     } else if (row < nvec) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<float4*>(slot + part_at(row, w * HC + c0 + i)) =
+                            *reinterpret_cast<float4*>(slot + part_at(row, c0 + i)) =
                                 make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                     }
                 }
@@ -521,8 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
 #pragma unroll 4
                     for (int i = e256; i < nvec * (D / 8); i += kSoftmax) {
                         const int v = i / (D / 8), c = (i % (D / 8)) * 8;
-                        const uint4 u = *reinterpret_cast<const uint4*>(
-                            (const uint8_t*)(join + ((c / HC ^ 1) * 128 + v) * C::HLD + (c % HC & ~31)) + (c & 31) * 2);
+                        const uint4 u = *reinterpret_cast<const uint4*>(join + v * C::QLD + c * 2);
                         const int vr = v * p.g_magic >> 16;
                         *reinterpret_cast<uint4*>(out0 + ((size_t)vr * p.nq + (v - vr * p.G)) * D + c) = u;
                     }
@@ -530,62 +529,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                     *reinterpret_cast<float2*>(slot + 2 * row) = make_float2(B, L);
                 }
             } else {
-                // group 1's O to shared memory, group 0 adds its own
-                if (w == 1) {
+                // the copies of a vector have bases and sums of their own
+                float* jf = reinterpret_cast<float*>(join);
 #pragma unroll 1
-                    for (int c0 = 0; c0 < D; c0 += 32) {
-                        float v[32];
-                        tmem_ld32w(my_o + c0, v);
+                for (int c0 = w * HC; c0 < (w + 1) * HC; c0 += 32) {
+                    float v[32];
+                    tmem_ld32w(my_o + c0, v);
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<float4*>(join + rl * C::OLD + c0 + i) =
-                                last >= 0 ? make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    }
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<float4*>(jf + rl * C::OLD + c0 + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                 }
-                named_bar_sync(1, kSoftmax);
-                if (w == 0) {
-                    const float2 other = ml[128 + rl];
-                    const float B = fmaxf(base, other.x), z = B == -INFINITY ? 0.f : B;
-                    const float f0 = pow2_int(base - z), f1 = pow2_int(other.x - z);
-#pragma unroll 1
-                    for (int c0 = 0; c0 < D; c0 += 32) {
-                        float v[32];
-                        tmem_ld32w(my_o + c0, v);
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            float4* d4 = reinterpret_cast<float4*>(join + rl * C::OLD + c0 + i);
-                            float4 o = *d4;
-                            o.x = (last >= 0 ? f0 * v[i] : 0.f) + f1 * o.x;
-                            o.y = (last >= 0 ? f0 * v[i + 1] : 0.f) + f1 * o.y;
-                            o.z = (last >= 0 ? f0 * v[i + 2] : 0.f) + f1 * o.z;
-                            o.w = (last >= 0 ? f0 * v[i + 3] : 0.f) + f1 * o.w;
-                            *d4 = o;
-                        }
-                    }
-                    ml[rl] = make_float2(B, f0 * l + f1 * other.y);
-                }
+                named_bar_sync(1, kSoftmax);             // all have read the groups' sums
+                if (w == 0) ml[rl] = make_float2(B, L);
                 named_bar_sync(1, kSoftmax);
                 // rows in order for the output, columns in order for a partial
 #pragma unroll 1
                 for (int i = e256; i < RW * (D / 8); i += kSoftmax) {
                     const int v = whole ? i / (D / 8) : i % RW, c = (whole ? i % (D / 8) : i / RW) * 8;
                     if (v >= nvec) continue;
-                    float B = -INFINITY, L = 0.f, a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    float Bv = -INFINITY, Lv = 0.f, a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int k = 0; k < CS; ++k) B = fmaxf(B, ml[v + k * RW].x);
-                    const float z = B == -INFINITY ? 0.f : B;
+                    for (int k = 0; k < CS; ++k) Bv = fmaxf(Bv, ml[v + k * RW].x);
+                    const float zv = Bv == -INFINITY ? 0.f : Bv;
 #pragma unroll
                     for (int k = 0; k < CS; ++k) {
                         const float2 m = ml[v + k * RW];
-                        const float f = pow2_int(m.x - z);
-                        const float4 w0 = *reinterpret_cast<const float4*>(join + (v + k * RW) * C::OLD + c);
-                        const float4 w1 = *reinterpret_cast<const float4*>(join + (v + k * RW) * C::OLD + c + 4);
-                        L += f * m.y;
+                        const float f = pow2_int(m.x - zv);
+                        const float4 w0 = *reinterpret_cast<const float4*>(jf + (v + k * RW) * C::OLD + c);
+                        const float4 w1 = *reinterpret_cast<const float4*>(jf + (v + k * RW) * C::OLD + c + 4);
+                        Lv += f * m.y;
                         a[0] += f * w0.x; a[1] += f * w0.y; a[2] += f * w0.z; a[3] += f * w0.w;
                         a[4] += f * w1.x; a[5] += f * w1.y; a[6] += f * w1.z; a[7] += f * w1.w;
                     }
                     if (whole) {
-                        const float inv = L == 0.f ? 0.f : 1.0f / L;
+                        const float inv = Lv == 0.f ? 0.f : 1.0f / Lv;
                         __nv_bfloat16* dst = (__nv_bfloat16*)p.out +
                                              ((size_t)(e.y + s.r0 + v / p.G) * p.nq + (size_t)s.g * p.G + v % p.G) * D + c;
                         *reinterpret_cast<uint4*>(dst) =
@@ -594,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                     } else {
                         *reinterpret_cast<float4*>(slot + part_at(v, c)) = make_float4(a[0], a[1], a[2], a[3]);
                         *reinterpret_cast<float4*>(slot + part_at(v, c + 4)) = make_float4(a[4], a[5], a[6], a[7]);
-                        if (c == 0) *reinterpret_cast<float2*>(slot + 2 * v) = make_float2(B, L);
+                        if (c == 0) *reinterpret_cast<float2*>(slot + 2 * v) = make_float2(Bv, Lv);
                     }
                 }
             }
@@ -602,7 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                 rec[0] = make_int4(line_owner(s.v0 + kOverhead + s.span.nt - 1, U, P), nvec, e.y + s.r0, s.g);
             }
             it0 += s.t1 - s.t0;
-            named_bar_sync(1, kSoftmax);      // join and ml are free again
+            tc_fence_before();
+            named_bar_sync(1, kSoftmax);      // O, join and ml are free again
         }
     }
     tc_fence_before();
@@ -617,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
 // the item whose first tile CTA c held, and adds the partials of CTAs c .. rec.x in order.
 template <int D>
 __global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ PagedAttnParams p) {
-    constexpr int SLOT = BlockCfg<D>::SLOT;
+    constexpr int SLOT = kSlot<D>;
     griddep_wait();
     griddep_launch();
     const int c0 = blockIdx.x;
@@ -665,9 +643,9 @@ __global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ Page
 template <int D, int CS>
 int launch_dc(const PagedAttnParams& p, int num_sms, cudaStream_t st) {
     auto kern = k_paged_block<D, CS>;
-    if (!allow_smem<D * 8 + CS>((const void*)kern, BlockCfg<D>::SMEM)) return 1;
+    if (!allow_smem<D * 8 + CS>((const void*)kern, (BlockCfg<D, CS>::SMEM))) return 1;
     const int ctas = std::min(num_sms, kPagedCtas), pieces = p.rt * p.G * (D / 8);
-    cudaError_t e = launch_k(kern, dim3(ctas), dim3(kThreads), BlockCfg<D>::SMEM, st, p);
+    cudaError_t e = launch_k(kern, dim3(ctas), dim3(kThreads), (BlockCfg<D, CS>::SMEM), st, p);
     if (e == cudaSuccess) e = launch_k(k_paged_join<D>, dim3(ctas, (pieces + 255) / 256), dim3(256), 0, st, p);
     return (int)e;
 }
