@@ -421,6 +421,31 @@ DF_DEV bool mbar_wait_short(uint64_t* bar, uint32_t parity, volatile int* abort_
         }
     }
 }
+// The same for a converged warp, whose lanes leave together: branches on votes only.
+DF_DEV bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+            : "memory");
+        if (__all_sync(0xffffffffu, ok)) return true;
+        if ((it & 31u) == 0) {
+            if (__any_sync(0xffffffffu, *abort_flag)) return false;
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (__any_sync(0xffffffffu, now - t0 > kWaitLimitNs)) {
+                *abort_flag = 1;
+                if (status) atomicCAS(status, 0, DFLASH_TIMEOUT);
+                return false;
+            }
+        }
+    }
+}
 DF_DEV int atom_add_acq_rel(int* p, int v) {
     int old;
     asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");

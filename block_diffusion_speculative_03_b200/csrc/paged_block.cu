@@ -200,11 +200,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                     wanted = __ballot_sync(0xffffffffu, row >= 0);
                 }
                 const int n_want = __popc((wanted >> (j * boxes)) & tile_boxes);
-                ok = mbar_wait_short(&empty[st], (uint32_t)(((it / S) & 1) ^ 1), abort_flag, p.wait_status);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
+                ok = mbar_wait_warp(&empty[st], (uint32_t)(((it / S) & 1) ^ 1), abort_flag, p.wait_status);
+                if (!ok) break;
                 if (tile_of == j) {
                     if (b == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(n_want * box_rows * 128 * C::HALVES));
                     if (row >= 0) {
@@ -223,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                 if (t - s.t0 >= S && staged < 128) stage_some(staged + 16);
             }
             if (more && ok) {
-                ok = __all_sync(0xffffffffu, mbar_wait_short(q_full, (uint32_t)(seg & 1), abort_flag, p.wait_status));
+                ok = mbar_wait_warp(q_full, (uint32_t)(seg & 1), abort_flag, p.wait_status);
                 if (!ok) break;
                 stage_some(128);
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(q_staged)) : "memory");
@@ -245,13 +242,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
         int it = 0, seg = 0;
         bool ok = true;
         for (; ok && walk.next(line, s); ++seg) {
-            ok = __all_sync(0xffffffffu, mbar_wait_short(q_full, (uint32_t)(seg & 1), abort_flag, p.wait_status));
+            ok = mbar_wait_warp(q_full, (uint32_t)(seg & 1), abort_flag, p.wait_status);
             for (int t = s.t0; t < s.t1 && ok; ++t, ++it) {
                 const int st = it % S;
-                ok = mbar_wait_short(&kv_full[st], (uint32_t)((it / S) & 1), abort_flag, p.wait_status);
+                ok = mbar_wait_warp(&kv_full[st], (uint32_t)((it / S) & 1), abort_flag, p.wait_status);
                 if (ok && it >= kBufs)
-                    ok = mbar_wait_short(&pv_done[it % kBufs], (uint32_t)((it / kBufs - 1) & 1), abort_flag, p.wait_status);
-                ok = __all_sync(0xffffffffu, ok);
+                    ok = mbar_wait_warp(&pv_done[it % kBufs], (uint32_t)((it / kBufs - 1) & 1), abort_flag, p.wait_status);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t ka = smem_u32(ring + st * C::KV), d = tS + (it % kBufs) * 64;
@@ -281,9 +277,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
         while (ok && walk.next(line, s)) {
             for (int t = s.t0; t < s.t1; ++t, ++it) {
                 const int sb = it % kBufs;
-                ok = mbar_wait_short(&kv_full[S + it % S], (uint32_t)((it / S) & 1), abort_flag, p.wait_status);
-                if (ok) ok = mbar_wait_short(&p_full[sb], (uint32_t)((it / kBufs) & 1), abort_flag, p.wait_status);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = mbar_wait_warp(&kv_full[S + it % S], (uint32_t)((it / S) & 1), abort_flag, p.wait_status);
+                if (ok) ok = mbar_wait_warp(&p_full[sb], (uint32_t)((it / kBufs) & 1), abort_flag, p.wait_status);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t va = smem_u32(ring + (S + it % S) * C::KV), a = tS + sb * 64;
@@ -316,8 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
         // tile's vectors take whatever stands there (their rows are not written)
         auto put_q = [&](int n) -> bool {
             if (n > 0) {
-                const bool got = mbar_wait_short(q_staged, (uint32_t)((n - 1) & 1), abort_flag, p.wait_status);
-                if (!__all_sync(0xffffffffu, got)) return false;
+                if (!mbar_wait_warp(q_staged, (uint32_t)((n - 1) & 1), abort_flag, p.wait_status)) return false;
             }
             const uint8_t* src = q_stage + row * C::QLD;
 #pragma unroll 1
@@ -365,8 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                 const int it = it0 + t - s.t0;
                 const int sb = it % kBufs;
                 const uint32_t my_s = tS + lanes + sb * 64;            // S, then P
-                ok = mbar_wait_short(&s_full[sb], (uint32_t)((it / kBufs) & 1), abort_flag, p.wait_status);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = mbar_wait_warp(&s_full[sb], (uint32_t)((it / kBufs) & 1), abort_flag, p.wait_status);
                 if (!ok) break;
                 tc_fence_after();
                 const int k0 = s.span.tile(t) * 64, kvb = k0 + col;
@@ -387,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                     }
                     // V rows that no row sees may hold anything (0 * NaN is NaN): zero them
                     if (k0 + 64 > hi_tile || (k0 < lo_tile && k0 + 64 > p.sinks)) {
-                        mbar_wait_short(&kv_full[S + it % S], (uint32_t)((it / S) & 1), abort_flag, p.wait_status);
+                        mbar_wait_warp(&kv_full[S + it % S], (uint32_t)((it / S) & 1), abort_flag, p.wait_status);
                         // two threads to a row
                         const int k = k0 + (rl >> 1);
                         if (k >= hi_tile || (k < lo_tile && k >= p.sinks)) {
@@ -407,8 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                 const float nb = floorf(fmax3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * p.scale_log2);
                 // the base that the tile before left (the other group's, half a turn ago), and this tile's
                 if (t > s.t0) {
-                    ok = mbar_wait_short(&base_set[w ^ 1], (uint32_t)(((it - 1) >> 1) & 1), abort_flag, p.wait_status);
-                    ok = __all_sync(0xffffffffu, ok);
+                    ok = mbar_wait_warp(&base_set[w ^ 1], (uint32_t)(((it - 1) >> 1) & 1), abort_flag, p.wait_status);
                     if (!ok) break;
                     const float before = base_s[(w ^ 1) * 128 + rl];
                     if (before != base) {
@@ -424,9 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                 mbar_arrive_if(lane == 0, &base_set[w]);
                 if (__any_sync(0xffffffffu, grow) && t > s.t0) {
                     // O holds the tiles before: once their products are done
-                    ok = mbar_wait_short(&pv_done[(it - 1) % kBufs], (uint32_t)(((it - 1) / kBufs) & 1), abort_flag,
+                    ok = mbar_wait_warp(&pv_done[(it - 1) % kBufs], (uint32_t)(((it - 1) / kBufs) & 1), abort_flag,
                                          p.wait_status);
-                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after();
                     const float f = grow ? pow2_int(held - base) : 1.0f;
@@ -475,14 +466,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             mbar_arrive_if(lane == 0, q_free);
             more = walk.next(line, nx);
             if (ok && more && w == 0) {
-                ok = mbar_wait_short(q_free, (uint32_t)(seg & 1), abort_flag, p.wait_status);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = mbar_wait_warp(q_free, (uint32_t)(seg & 1), abort_flag, p.wait_status);
                 if (ok) ok = put_q(seg + 1);
             }
             ++seg;
             {
                 const int last = it0 + s.t1 - s.t0 - 1;
-                if (ok) ok = mbar_wait_short(&pv_done[last % kBufs], (uint32_t)((last / kBufs) & 1), abort_flag, p.wait_status);
+                if (ok) ok = mbar_wait_warp(&pv_done[last % kBufs], (uint32_t)((last / kBufs) & 1), abort_flag, p.wait_status);
             }
             ml[w * 128 + rl] = make_float2(base, l);
             if (named_bar_or(1, kSoftmax, !ok)) break;

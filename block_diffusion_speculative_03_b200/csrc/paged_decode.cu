@@ -121,11 +121,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
                 const int b = lane & (boxes - 1), kind = lane / boxes, kb = k0 + b * box_rows;
                 const bool want = kind < 2 && kb < hi && (kb < p.sinks || kb + box_rows > lo);
                 const int page = look.at(p, e.x, k0, kb, boxes, lane);
-                ok = mbar_wait_short(&empty[st], (uint32_t)(((it / S) & 1) ^ 1), abort_flag, p.wait_status);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
+                ok = mbar_wait_warp(&empty[st], (uint32_t)(((it / S) & 1) ^ 1), abort_flag, p.wait_status);
+                if (!ok) break;
                 const int n_want = __popc(__ballot_sync(0xffffffffu, want && page >= 0));
                 if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(n_want * box_rows * D * 2));
                 __syncwarp();
@@ -188,8 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
 
         for (int t = s.t0 + ((it0 ^ group) & 1); t < s.t1; t += 2) {
             const int it = it0 + t - s.t0, st = it % S;
-            if (ok) ok = mbar_wait_short(&full[st], (uint32_t)((it / S) & 1), abort_flag, p.wait_status);
-            ok = __all_sync(0xffffffffu, ok);
+            if (ok) ok = mbar_wait_warp(&full[st], (uint32_t)((it / S) & 1), abort_flag, p.wait_status);
             if (!ok) continue;
             const int kw = s.span.tile(t) * kTileKeys + cw * 16;          // this warp's first key
             const uint32_t sk = ring_a + st * 2 * C::TILE, sv = sk + C::TILE;
