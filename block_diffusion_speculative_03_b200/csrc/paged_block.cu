@@ -29,7 +29,7 @@ namespace df {
 
 namespace {
 
-constexpr int kOverhead = 10;   // units that starting and ending an item costs, in tiles
+constexpr int kOverhead = 8;    // units that starting and ending an item costs, in tiles
 constexpr int kMinShare = 8;   // smallest share of a CTA, in units
 
 constexpr int kThreads = 384;
