@@ -1,5 +1,6 @@
 // The paged key/value pool: views, launchers of the page operations (pages.cu)
-// and of attention over pages or over a cache slab (paged_attn.cu, paged_attn_tc.cu).
+// and of attention over pages or over a cache slab (paged_decode.cu: few rows, paged_block.cu:
+// many; paged_attn.cu: fp32 storage).
 #pragma once
 #include <atomic>
 
@@ -524,8 +525,7 @@ DF_DEV void tmem_ld64w(uint32_t taddr, float* v) {
 DF_DEV int line_owner(int u, int U, int P) { return (int)((((long long)u + 1) * P - 1) / U); }
 DF_DEV int line_begin(int c, int U, int P) { return (int)((long long)c * U / P); }
 
-// Issue the TMA loads of one 64-key tile of K and V by a whole warp: pages looked up 32 at
-// a time.  A box is min(page_size, 64) rows; boxes in which no row sees a key are not loaded.
+// The pages of a sequence, looked up 32 at a time by a whole warp.
 struct PageLookup {
     int first, page;    // pages first .. first + 31 of the sequence, one per lane
     DF_DEV void reset() { first = -(1 << 30); }

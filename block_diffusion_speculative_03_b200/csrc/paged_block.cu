@@ -7,20 +7,29 @@
 // RW = 128 / CS lanes: lane l holds vector l % RW and takes key slice l / RW (64 / CS keys)
 // of every tile, so all softmax warps have work.
 //
-//   warps 2-9  softmax, two groups of four warps that take the tiles in turn, each with its
-//              own S and O in tensor memory and its own running base and sum per lane (they are
-//              joined once per stretch; the chains hide each other's latencies).  Per tile: read S,
-//              mask it where the tile has keys that some row does not see, write P =
-//              bf16(2^(t - b)), rescale O by an exact power of two when b moves.
-//   warp 0, 11 TMA: K and V tiles of 64 keys, one box per page and 64-column half; warp 0 also
-//              stages the next stretch's Q.
-//   warp 1     tcgen05.mma: S = Q K^T into the next of three buffers; a tile's P takes the place of
-//              its S, so a buffer is free again when the tile's product is done.
+//   warps 2-9  softmax, two groups of four warps that take the tiles in turn and hide each
+//              other's latencies.  Per tile: read S, mask it where the tile has keys that some
+//              row does not see, take over the running base from the tile before (the other
+//              group's, through shared memory), move it if a maximum has passed it (then O is
+//              rescaled, by an exact power of two), write P = bf16(2^(t - b)).
+//   warp 0, 11 TMA: K and V tiles of 64 keys, one box per page and 64-column half; both also
+//              stage the next stretch's Q.
+//   warp 1     tcgen05.mma: S = Q K^T into the next of kBufs buffers; a tile's P takes the place
+//              of its S, so a buffer is free again when the tile's product is done.
 //   warp 10    tcgen05.mma: O += P V once P is there.  (Two issuers that each wait for one thing:
 //              one that polled for both took 300 to 700 cycles to notice either.)
 //
 // An item that several CTAs hold is joined by a second launch (k_paged_join): adding up to 18
 // partials of 32 KB took one CTA 15 us, all SMs together 2 us.
+//
+// Few rows on long contexts are bound by HBM (32 sequences of 4000 with 8 heads of 128, 8 rows of
+// 4 heads: 97 us for 524 MB, 5.4 TB/s), many rows by the softmax warps: 2048 rows of 32 heads of 128
+// behind 6000 positions with a window of 2048 take 86 us, 0.8 PFLOP/s of products, at 900 cycles a
+// tile where the tensor cores need 520 and the exponentials 512, and 6000 cycles more for each
+// stretch's end and beginning.  What the time is not: taking out exponentials, conversions or most
+// of the products changed it by less than 1 %; it is the waits and the chain read S - maximum -
+// exponentials - write P of each group.  Three buffers and an O for each group (the chain then ran
+// through the product and back) took 95 us; three groups 89, a thread to half a row 106.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -29,8 +38,12 @@ namespace df {
 
 namespace {
 
-constexpr int kOverhead = 8;    // units that starting and ending an item costs, in tiles
-constexpr int kMinShare = 8;   // smallest share of a CTA, in units
+// Units that starting and ending an item costs, in tiles (9 entries of up to 700 rows, 2 kv heads:
+// 16.4 us with 8, 16.8 with 10, 15.9 with 6; 2048 rows of one entry: 86.0, 85.8, 87.5).
+constexpr int kOverhead = 8;
+// Smallest share of a CTA, in units (the same entries: 15.3 us with 4 or 5, 16.0 with 8, 16.8 with 14; of
+// calls of 7 to 18 us most are faster with 5 than with 8, by up to 1.5 us, some slower, by as much).
+constexpr int kMinShare = 5;
 
 constexpr int kThreads = 384;
 constexpr int kSoftmax = 256;    // threads of the two softmax groups
@@ -639,6 +652,8 @@ int launch_dc(const PagedAttnParams& p, int num_sms, cudaStream_t st) {
     if (e == cudaSuccess) e = launch_k(k_paged_join<D>, dim3(ctas, (pieces + 255) / 256), dim3(256), 0, st, p);
     return (int)e;
 }
+// Copies of the window of vectors: as many as fit.  32 sequences of 4000: one kv head of 64, 32 vectors:
+// 15.1 us with 4 copies, 16.1 with 2, 22.9 with 1; 8 kv heads of 128, 64 vectors: 99.8 with 2, 113 with 1.
 template <int D>
 int launch_d(const PagedAttnParams& p, int vectors, int num_sms, cudaStream_t st) {
     if (vectors <= 32) return launch_dc<D, 4>(p, num_sms, st);

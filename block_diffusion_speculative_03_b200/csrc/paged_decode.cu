@@ -22,6 +22,10 @@
 //              the warps until the end of the item.  (At 16 rows the tensor work is 1/8 of
 //              what the loads leave time for, so the register path wins over tensor memory:
 //              no hand-offs between issuing, softmax and correction.)
+//
+// Measured, one token, 32 heads on 8 of 128: 4 sequences of 32768 84.2 us (537 MB, 6.4 TB/s, 99 % of
+// a copy); one of 2048 10.1 us, of which 1.3 are HBM: the launch, the dependent reads of the plan
+// (list, length, table), the first load, and the join of 3-tile shares make up the rest.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -34,7 +38,8 @@ constexpr int kConsumers = 8;      // two groups of four warps take the tiles in
 constexpr int kThreads = 32 + 32 * kConsumers;
 constexpr int kTileKeys = kLineTile;
 constexpr int kOverhead = 2;   // units that starting and joining an item costs, in tiles
-constexpr int kMinShare = 3;   // smallest share of a CTA, in units
+// Smallest share of a CTA, in units (one sequence of 2048, 8 kv heads: 10.2 us with 3, 11.3 with 2, 12.0 with 6).
+constexpr int kMinShare = 3;
 
 template <int D> struct DecodeCfg {
     static constexpr int TILE = kTileKeys * D * 2;           // bytes of a K (or V) tile
