@@ -168,6 +168,42 @@ def test_side_stream():
         check_rows(out[s:s + 1], q[s:s + 1], model.rows_of(s, n)[0], n - 1, n, 64, torch.bfloat16)
 
 
+def test_two_pools_on_two_streams():
+    """Calls of different pools at once: tokens, blocks and page operations beside one another."""
+    torch.manual_seed(5)
+    pools, calls, want = [], [], []
+    for k in range(2):
+        pool, _ = make_pool("bf16", 1, 8, 2, 128, 400, 16, 5, 1500, seed=k)
+        pool.reserve(i32([1200, 40, 700, 3]))
+        pool.advance(i32([1184, 24, 684, 0]))
+        qa, qb = torch.randn(4, 8, 128, device="cuda").bfloat16(), torch.randn(64, 8, 128, device="cuda").bfloat16()
+        oa, ob = torch.empty_like(qa), torch.empty_like(qb)
+        args = (i32([0, 1, 2, 3]), i32([0, 16, 32, 48]), i32([16, 16, 16, 3]))
+        src, dst = i32([2]), i32([4])
+
+        def call(pool=pool, qa=qa, qb=qb, oa=oa, ob=ob, args=args, src=src, dst=dst):
+            pool.attention(0, qb, ob, *args, 16, window=500, sinks=4)
+            pool.attention(0, qa, oa, args[0])
+            pool.fork(src, dst, deep=True)
+            pool.free(dst)
+
+        call()
+        pools.append(pool)
+        calls.append(call)
+        want.append((oa, oa.clone(), ob, ob.clone()))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    for _ in range(30):
+        for st, call in zip(streams, calls):
+            with torch.cuda.stream(st):
+                call()
+    torch.cuda.synchronize()
+    for pool, (oa, wa, ob, wb) in zip(pools, want):
+        assert pool.status() == 0
+        assert torch.equal(oa, wa) and torch.equal(ob[:51], wb[:51])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("rows", [1, 3, 40])
 def test_many_entries_of_few_sequences(dtype, rows):
@@ -192,6 +228,60 @@ def test_many_entries_of_few_sequences(dtype, rows):
         else:
             s = seqs[i]
             check_rows(out[mine], q[mine], model.rows_of(s, lens[s] + rows)[0], lens[s], lens[s] + rows, d, DT[dtype])
+
+
+@pytest.mark.parametrize("nq,nkv,d,rows", [(8, 2, 128, 4), (8, 2, 64, 8), (8, 2, 128, 16), (8, 2, 64, 16),
+                                           (8, 2, 128, 60), (12, 4, 64, 43)])
+@pytest.mark.parametrize("ctx", [300, 6000])
+@pytest.mark.parametrize("window", [0, 170])
+def test_rising_and_falling_scores(nq, nkv, d, rows, ctx, window):
+    """The running maximum of some rows rises by 2^50 every 64 keys, of others it falls: every tile moves
+    bases, in each of the kernels' row layouts, within a share and across shares."""
+    pool, _ = make_pool("bf16", 1, nq, nkv, d, 120, 64, 1, ctx + rows)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(rows)
+    slab = pool.slab()
+    pool.reserve(i32([ctx + rows]))
+    pool.advance(i32([ctx]))
+    n = ctx + rows
+    k = torch.randn(nkv, n, d, device="cuda", generator=g)
+    ramp = torch.arange(n, device="cuda") // 8 * (4.0 if ctx < 1000 else 0.5)      # scores: times q[.., 0] / sqrt(d)
+    k[:, :, 0] = ramp
+    v = torch.randn(nkv, n, d, device="cuda", generator=g)
+    q = torch.randn(rows, nq, d, device="cuda", generator=g)
+    q[:, :, 0] = torch.where(torch.rand(rows, nq, device="cuda", generator=g) < 0.5, 1.0, -1.0) * d ** 0.5
+    pages = pool.table[0, :M.ceil_div(n, 64)].long()
+    for kind, x in ((0, k), (1, v)):
+        x = torch.nn.functional.pad(x, (0, 0, 0, len(pages) * 64 - n)).unflatten(1, (-1, 64)).transpose(0, 1)
+        slab[pages, 0, kind] = x.bfloat16()
+    kv = slab[pages, 0].permute(1, 2, 0, 3, 4).flatten(2, 3)[:, :, :n]
+    q = q.bfloat16()
+    out = pool.attention(0, q, None, i32([0]), i32([0]), i32([rows]), rows, True, window, 3)
+    assert pool.status() == 0 and torch.isfinite(out.float()).all()
+    check_rows(out, q, kv, ctx, n, d, torch.bfloat16, True, window, 3)
+
+
+@pytest.mark.parametrize("rows", [4, 8, 16, 50])
+@pytest.mark.parametrize("bad", ["nan", "inf"])
+def test_bad_keys_stay_in_the_rows_that_see_them(rows, bad):
+    """A key of the call's own rows that is not a number: the rows before it do not see it."""
+    pool, model = make_pool("bf16", 1, 8, 2, 128, 40, 16, 2, 400)
+    ctx, at = 250, rows // 2
+    pool.reserve(i32([ctx + rows, ctx + rows]))
+    pool.advance(i32([ctx, ctx]))
+    model.reserve([0, 1], [ctx + rows] * 2)
+    slab = pool.slab()
+    page = pool.table[0, (ctx + at) // 16].item()
+    slab[page, 0, 0, 1, (ctx + at) % 16] = float(bad)
+    q = torch.randn(2 * rows, 8, 128, device="cuda").bfloat16()
+    out = pool.attention(0, q, None, None, i32([0, rows]), i32([rows, rows]), rows)
+    for s in range(2):
+        kv = model.rows_of(s, ctx + rows)[0]           # (the model's rows are as they were before)
+        good = at if s == 0 else rows
+        check_rows(out[s * rows:s * rows + good], q[s * rows:s * rows + good], kv, ctx, ctx + rows, 128, torch.bfloat16)
+    assert torch.isfinite(out[at:rows, :4].float()).all()          # the other kv head
+    seen = out[at:rows, 4:].float()
+    assert torch.isnan(seen).any() if bad == "inf" else torch.isnan(seen).all()
 
 
 def test_large_pool_and_long_context():
