@@ -98,25 +98,31 @@ DF_DEV int pages_for(long long positions, int ps_log2) {
 // ---------------------------------------------------------------------------
 // reserve, deep fork: plan
 // ---------------------------------------------------------------------------
-// Entry i wants the table indices [first, past) of its sequence (`sid`).  reserve:
-// an index needs a new page when it has none, or when its page has more holders
-// than the entries of this call up to and including this one that write it (those
-// before it in the list have taken copies).  deep fork: every index needs one.
+// Entry i wants the table indices [first, past) of its sequence (`sid`).  reserve: an index needs a
+// new page when it has none, or when others hold its page too, but for one case: when all holders
+// of a page are entries of this call that write it, the last of them keeps it.  So per shared page
+// the writers are counted and the last is found: two atomics an index (128 forks of one page, all
+// reserved at once: 16 us, against 77 with every entry searching the ones before it; 1023: 89,
+// against 6900).  deep fork: every index needs one.
 // Decisions are made twice (counted, then written) from the same tables, which stay as they are
 // until all are made: no list of candidates has to fit anywhere.
 template <bool FORK>
 __global__ void __launch_bounds__(kPlan) k_pages_plan(PoolView v, const int* __restrict__ seqs,
                                                       const int* __restrict__ grow, const int* __restrict__ src, int n) {
     __shared__ int sid[kPoolMaxSeqs], first[kPoolMaxSeqs], past[kPoolMaxSeqs], cnt[kPoolMaxSeqs];
+    __shared__ int owner[kPoolMaxSeqs];      // the first entry that lists a sequence
     __shared__ int sums[33];
     griddep_wait();
     griddep_launch();
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     if (t == 0) *v.n_copies = 0;
+    owner[t] = kPlan;
+    __syncthreads();
     if (t < n) {
         const int s = entry_seq(v, seqs, t);
         sid[t] = s;
         first[t] = past[t] = 0;
+        if (s >= 0) atomicMin(&owner[s], t);
     }
     __syncthreads();
     if (t < n) {
@@ -124,8 +130,7 @@ __global__ void __launch_bounds__(kPlan) k_pages_plan(PoolView v, const int* __r
         if (s == -2) {
             err = DFLASH_INVALID_ARG;
         } else if (s >= 0) {
-            for (int j = 0; j < t; ++j)
-                if (sid[j] == s) err = DFLASH_INVALID_ARG;
+            if (owner[s] < t) err = DFLASH_INVALID_ARG;
             if (FORK) {
                 const int a = src[t];
                 if (a == -1) {
@@ -156,17 +161,37 @@ __global__ void __launch_bounds__(kPlan) k_pages_plan(PoolView v, const int* __r
     }
     __syncthreads();
 
+    // (writers, last writer) of the shared pages stand in v.copies until the decisions are made
     auto needs_new = [&](int i, int c) -> bool {
         if (FORK) return true;
         const int x = v.table[(size_t)sid[i] * v.max_pages + c];
         if (x < 0) return true;
         const int holders = v.refs[x];
         if (holders <= 1) return false;
-        int before = 0;
-        for (int j = 0; j < i; ++j)
-            before += c >= first[j] && c < past[j] && v.table[(size_t)sid[j] * v.max_pages + c] == x;
-        return holders - before > 1;
+        return !(__ldcg(&v.copies[x].x) == holders && __ldcg(&v.copies[x].y) == i);
     };
+    if (!FORK) {
+        bool shared = false;
+        for (int i = warp; i < n; i += kPlan / 32)
+            for (int c = first[i] + lane; c < past[i]; c += 32) {
+                const int x = v.table[(size_t)sid[i] * v.max_pages + c];
+                if (x >= 0 && v.refs[x] > 1) {
+                    shared = true;
+                    v.copies[x] = make_int4(0, -1, 0, 0);
+                }
+            }
+        if (__syncthreads_or(shared)) {
+            for (int i = warp; i < n; i += kPlan / 32)
+                for (int c = first[i] + lane; c < past[i]; c += 32) {
+                    const int x = v.table[(size_t)sid[i] * v.max_pages + c];
+                    if (x >= 0 && v.refs[x] > 1) {
+                        atomicAdd(&v.copies[x].x, 1);
+                        atomicMax(&v.copies[x].y, i);
+                    }
+                }
+            __syncthreads();
+        }
+    }
     for (int i = warp; i < n; i += kPlan / 32) {
         int total = 0;
         for (int c0 = first[i]; c0 < past[i]; c0 += 32)
@@ -504,8 +529,9 @@ __global__ void k_tables_apply(PoolView v, const int* lens, const int* table) {
 }
 
 // The three steps in one block, for tables that it goes through faster than two more launches
-// take (1024 entries: 2.7 us against 3.5; 2048: 3.8 both; 8192: 9.5 against 4.0).
-constexpr int kSmallTables = 2048;
+// take (1024 entries: 2.7 us against 3.5 on the device; 2048: 3.8 both; 4096: 5.5 against 4.0, which
+// the host pays for with two more launches; 8192: 9.5).
+constexpr int kSmallTables = 4096;
 __global__ void __launch_bounds__(kPlan) k_tables_small(PoolView v, const int* lens, const int* table) {
     griddep_wait();
     griddep_launch();
@@ -594,13 +620,17 @@ __global__ void __launch_bounds__(kPlan) k_pages_advance(PoolView v, const int* 
                                                          const int* __restrict__ row_count, int n) {
     griddep_wait();
     griddep_launch();
+    __shared__ int owner[kPoolMaxSeqs];      // the first entry that lists a sequence
     const int t = threadIdx.x;
-    if (t >= n) return;
-    const int s = entry_seq(v, seqs, t);
+    owner[t] = kPlan;
+    __syncthreads();
+    const int s = t < n ? entry_seq(v, seqs, t) : -1;
+    if (s >= 0) atomicMin(&owner[s], t);
+    __syncthreads();
     if (s == -1) return;
     const int c = row_count ? row_count[t] : 1;
     int err = 0;
-    if (s == -2 || c < 0 || listed_before(seqs, t, s, 0, 1)) {
+    if (s == -2 || c < 0 || owner[s] < t) {
         err = DFLASH_INVALID_ARG;
     } else if (c > 0) {
         const long long to = (long long)v.len[s] + c;

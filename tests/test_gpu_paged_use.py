@@ -168,6 +168,32 @@ def test_side_stream():
         check_rows(out[s:s + 1], q[s:s + 1], model.rows_of(s, n)[0], n - 1, n, 64, torch.bfloat16)
 
 
+@pytest.mark.parametrize("n,left_out", [(9, []), (9, [3]), (1023, []), (1023, [0, 700])])
+def test_wide_forks_write_at_once(n, left_out):
+    """Every holder of a shared page reserves in one call, in a shuffled order: all but the last copy
+    it, or all of them when a holder stands aside."""
+    pool, model = make_pool("bf16", 1, 2, 1, 64, 3 * n + 40, 16, n + 1, 80)
+    pool.reserve(i32([40]), i32([0]))
+    model.reserve([0], [40])
+    pool.advance(i32([37]), i32([0]))
+    model.advance([0], [37])
+    pool.fork(i32([0] * n), i32(list(range(1, n + 1))))
+    model.fork([0] * n, list(range(1, n + 1)))
+    g = torch.Generator()
+    g.manual_seed(n)
+    order = [s for s in torch.randperm(n + 1, generator=g).tolist() if s not in left_out]
+    grow = [(s * 7) % 25 for s in order]
+    pool.reserve(i32(grow), i32(order))
+    model.reserve(order, grow)
+    same(pool, model, "reserve")
+    counts = [min(x, 9) for x in grow]
+    if left_out:                                            # (room for a sequence that is listed twice)
+        order, counts = order + order[:1], counts + [1]
+    pool.advance(i32(counts), i32(order))
+    model.advance(order, counts)
+    same(pool, model, "advance")
+
+
 def test_two_pools_on_two_streams():
     """Calls of different pools at once: tokens, blocks and page operations beside one another."""
     torch.manual_seed(5)
