@@ -395,34 +395,10 @@ template <bool TILES> struct Walker {
     }
 };
 
-// Bounded wait on an mbarrier phase, as mbar_wait, for waits that are short and many: a try
-// may suspend the warp for up to 20 us (a warp that spins takes issue slots from the softmax
-// warps beside it), and the clock is first read after 32 of them.
-DF_DEV bool mbar_wait_short(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
-    uint64_t t0 = 0;
-    for (uint32_t it = 1;; ++it) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
-            : "memory");
-        if (ok) return true;
-        if ((it & 31u) == 0) {
-            if (*abort_flag) return false;
-            const uint64_t now = globaltimer_ns();
-            if (t0 == 0) t0 = now;
-            if (now - t0 > kWaitLimitNs) {
-                *abort_flag = 1;
-                if (status) atomicCAS(status, 0, DFLASH_TIMEOUT);
-                return false;
-            }
-        }
-    }
-}
-// The same for a converged warp, whose lanes leave together: branches on votes only.
+// Bounded wait on an mbarrier phase by a converged warp, as mbar_wait, for waits that are short and
+// many: a try may suspend the warp for up to 20 us (a warp that spins takes issue slots from the
+// softmax warps beside it), the clock is first read after 32 of them, and the lanes leave together,
+// by branches on votes only (lanes that leave one by one cost 100 cycles and more of reconvergence).
 DF_DEV bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
     uint64_t t0 = 0;
     for (uint32_t it = 1;; ++it) {
@@ -496,18 +472,6 @@ DF_DEV bool elect_one() {
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(r));
     return r != 0;
-}
-// Whether an mbarrier phase has completed, without waiting.
-DF_DEV bool mbar_test(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
 }
 // 32 lanes x 64 consecutive 32-bit columns of tensor memory, waited for in the same statement.
 DF_DEV void tmem_ld64w(uint32_t taddr, float* v) {

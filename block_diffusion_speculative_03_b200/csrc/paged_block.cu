@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
         if (!ok) {
             // an abandoned launch: its copies land before the CTA exits
             volatile int never = 0;
-            for (int k = max(0, it - S); k < it; ++k) mbar_wait_short(&full[k % S], (uint32_t)((k / S) & 1), &never, nullptr);
+            for (int k = max(0, it - S); k < it; ++k) mbar_wait_warp(&full[k % S], (uint32_t)((k / S) & 1), &never, nullptr);
             asm volatile("cp.async.wait_all;" ::: "memory");
         }
     } else if (warp == 1) {
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             if (leader) tc_commit(&drain[0]);   // the issued MMAs finish before the tensor memory is released
             __syncwarp();
             volatile int never = 0;
-            mbar_wait_short(&drain[0], 0, &never, nullptr);
+            mbar_wait_warp(&drain[0], 0, &never, nullptr);
         }
     } else if (warp == kPvWarp) {
         // ------------------------------------------------------------ O += P V
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             if (leader) tc_commit(&drain[1]);
             __syncwarp();
             volatile int never = 0;
-            mbar_wait_short(&drain[1], 0, &never, nullptr);
+            mbar_wait_warp(&drain[1], 0, &never, nullptr);
         }
     } else {
         // ------------------------------------------------------------ softmax

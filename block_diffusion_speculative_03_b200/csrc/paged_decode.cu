@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
         if (!ok) {
             // an abandoned launch: its copies land before the CTA exits
             volatile int never = 0;
-            for (int k = max(0, it - S); k < it; ++k) mbar_wait_short(&full[k % S], (uint32_t)((k / S) & 1), &never, nullptr);
+            for (int k = max(0, it - S); k < it; ++k) mbar_wait_warp(&full[k % S], (uint32_t)((k / S) & 1), &never, nullptr);
         }
         return;
     }
