@@ -148,8 +148,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
     const int P = min((int)gridDim.x, max(1, U / kMinShare));
     if (tid == 64) rec[0] = make_int4(-1, 0, 0, 0);      // no item to join from here, so far
     if (U == 0 || (int)blockIdx.x >= P) return;
+    const Shares shares(U, P);
     Walker<true> walk;
-    walk.start(line, line_begin(blockIdx.x, U, P), line_begin(blockIdx.x + 1, U, P));
+    walk.start(line, shares.begin(blockIdx.x), shares.begin(blockIdx.x + 1));
     Stretch s;
     uint32_t tmem = 0;
     if (warp > 0 && warp <= kPvWarp) {      // the producers do not wait for the tensor memory
@@ -579,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                 }
             }
             if (!whole && head && e256 == 0) {
-                rec[0] = make_int4(line_owner(s.v0 + kOverhead + s.span.nt - 1, U, P), nvec, e.y + s.r0, s.g);
+                rec[0] = make_int4(shares.owner(s.v0 + kOverhead + s.span.nt - 1), nvec, e.y + s.r0, s.g);
             }
             it0 += s.t1 - s.t0;
             tc_fence_before();

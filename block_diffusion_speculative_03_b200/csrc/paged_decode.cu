@@ -104,8 +104,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
     const int U = line_plan<kThreads, D>(p, line, line_mem, sums, kOverhead);
     const int P = min((int)gridDim.x, max(1, U / kMinShare));
     if (U == 0 || (int)blockIdx.x >= P) return;
+    const Shares shares(U, P);
     Walker<false> walk;
-    walk.start(line, line_begin(blockIdx.x, U, P), line_begin(blockIdx.x + 1, U, P));
+    walk.start(line, shares.begin(blockIdx.x), shares.begin(blockIdx.x + 1));
     Stretch s;
     const int bl = p.table ? min(p.ps_log2, 6) : 6;          // log2 rows of a TMA box
     const int box_rows = 1 << bl, boxes = kTileKeys >> bl;
@@ -320,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
         }
         if (!whole) {
             // the CTAs that hold the item's first and last tile
-            const int c0 = line_owner(s.v0 + kOverhead, U, P), c1 = line_owner(s.v0 + kOverhead + s.span.nt - 1, U, P);
+            const int c0 = shares.owner(s.v0 + kOverhead), c1 = shares.owner(s.v0 + kOverhead + s.span.nt - 1);
             named_bar_sync(1, kConsumers * 32);
             if (c_tid == 0) {
                 // releases the block's partial (the barrier above) and acquires the others'
