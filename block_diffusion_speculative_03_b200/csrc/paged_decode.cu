@@ -24,7 +24,7 @@
 //              no hand-offs between issuing, softmax and correction.)
 //
 // Measured, one token, 32 heads on 8 of 128: 4 sequences of 32768 84.2 us (537 MB, 6.4 TB/s, 99 % of
-// a copy); one of 2048 10.1 us, of which 1.3 are HBM: the launch, the dependent reads of the plan
+// a copy); one of 2048 9.7 us, of which 1.3 are HBM: the launch, the dependent reads of the plan
 // (list, length, table), the first load, and the join of 3-tile shares make up the rest.
 #include <algorithm>
 
@@ -38,7 +38,8 @@ constexpr int kConsumers = 8;      // two groups of four warps take the tiles in
 constexpr int kThreads = 32 + 32 * kConsumers;
 constexpr int kTileKeys = kLineTile;
 constexpr int kOverhead = 2;   // units that starting and joining an item costs, in tiles
-// Smallest share of a CTA, in units (one sequence of 2048, 8 kv heads: 10.2 us with 3, 11.3 with 2, 12.0 with 6).
+// Smallest share of a CTA, in units (one sequence of 2048, 8 kv heads: 9.7 us with 3; 1.1 more with 2, 1.8
+// more with 6).
 constexpr int kMinShare = 3;
 
 template <int D> struct DecodeCfg {
@@ -332,22 +333,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
             named_bar_sync(1, kConsumers * 32);
             if (flag_s) {
                 auto part = [&](int c) { return p.partial + (size_t)(2 * c + (c == c0 ? 1 : 0)) * C::SLOT; };
-                for (int x = c_tid; x < R * (D / 4); x += kConsumers * 32) {
-                    const int r = x / (D / 4), c = (x % (D / 4)) * 4;
-                    float B = -INFINITY, L = 0.f;
-                    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int k0 = c0; k0 <= c1; k0 += 8) {      // eight partials' loads in flight
+                // adds the partials of CTAs k, k + 1, .. k + 7, k + step, .. to (B, L, a)
+                auto gather = [&](int r, int c, int k, int step, float& B, float& L, float4& a) {
+                    for (int k0 = k; k0 <= c1; k0 += step) {      // eight partials' loads in flight
                         float2 ml[8];
                         float4 v[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float* q = part(min(k0 + k, c1));
-                            ml[k] = __ldcg(reinterpret_cast<const float2*>(q + 2 * r));
-                            v[k] = __ldcg(reinterpret_cast<const float4*>(q + 32 + r * D + c));
+                        for (int j = 0; j < 8; ++j) {
+                            const float* q = part(min(k0 + j, c1));
+                            ml[j] = __ldcg(reinterpret_cast<const float2*>(q + 2 * r));
+                            v[j] = __ldcg(reinterpret_cast<const float4*>(q + 32 + r * D + c));
                         }
                         float nb = B;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) nb = fmaxf(nb, ml[k].x);
+                        for (int j = 0; j < 8; ++j) nb = fmaxf(nb, ml[j].x);
                         const float z = nb == -INFINITY ? 0.f : nb, g = pow2_int(B - z);
                         B = nb;
                         L *= g;
@@ -356,19 +355,65 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
                         a.z *= g;
                         a.w *= g;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            if (k0 + k > c1) break;
-                            const float f = pow2_int(ml[k].x - z);
-                            L += f * ml[k].y;
-                            a.x += f * v[k].x;
-                            a.y += f * v[k].y;
-                            a.z += f * v[k].z;
-                            a.w += f * v[k].w;
+                        for (int j = 0; j < 8; ++j) {
+                            if (k0 + j > c1) break;
+                            const float f = pow2_int(ml[j].x - z);
+                            L += f * ml[j].y;
+                            a.x += f * v[j].x;
+                            a.y += f * v[j].y;
+                            a.z += f * v[j].z;
+                            a.w += f * v[j].w;
                         }
                     }
+                };
+                auto store = [&](int r, int c, float L, const float4& a) {
                     const float inv = L == 0.f ? 0.f : 1.0f / L;
-                    __nv_bfloat16* dst = (__nv_bfloat16*)p.out + ((size_t)(e.y + (r * p.g_magic >> 16)) * p.nq + (size_t)s.g * p.G + r - (r * p.g_magic >> 16) * p.G) * D + c;
+                    const int v = r * p.g_magic >> 16;
+                    __nv_bfloat16* dst = (__nv_bfloat16*)p.out +
+                                         ((size_t)(e.y + v) * p.nq + (size_t)s.g * p.G + r - v * p.G) * D + c;
                     *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+                };
+                const int E = R * (D / 4), teams = min(8, kConsumers * 32 / E);
+                if (c1 - c0 < 8 || teams < 2) {
+                    for (int x = c_tid; x < E; x += kConsumers * 32) {
+                        float B = -INFINITY, L = 0.f;
+                        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+                        gather(x / (D / 4), (x % (D / 4)) * 4, c0, 8, B, L, a);
+                        store(x / (D / 4), (x % (D / 4)) * 4, L, a);
+                    }
+                } else {
+                    // few rows, many partials: teams of threads take eight partials each in turn (one
+                    // sequence of 2048, 8 kv heads of 4 rows, 12 partials: 9.7 us, 10.1 without)
+                    const int team = c_tid / E, x = c_tid - team * E, r = x / (D / 4), c = (x % (D / 4)) * 4;
+                    float B = -INFINITY, L = 0.f;
+                    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (team < teams) {
+                        gather(r, c, c0 + team * 8, teams * 8, B, L, a);
+                        join_ml[c_tid] = make_float2(B, L);
+                        *reinterpret_cast<float4*>(join + c_tid * 4) = a;
+                    }
+                    named_bar_sync(1, kConsumers * 32);
+                    if (team == 0) {
+                        float M = B;
+                        for (int k = 1; k < teams; ++k) M = fmaxf(M, join_ml[k * E + x].x);
+                        const float z = M == -INFINITY ? 0.f : M, f0 = pow2_int(B - z);
+                        L *= f0;
+                        a.x *= f0;
+                        a.y *= f0;
+                        a.z *= f0;
+                        a.w *= f0;
+                        for (int k = 1; k < teams; ++k) {
+                            const float2 ml = join_ml[k * E + x];
+                            const float4 v = *reinterpret_cast<const float4*>(join + (k * E + x) * 4);
+                            const float f = pow2_int(ml.x - z);
+                            L += f * ml.y;
+                            a.x += f * v.x;
+                            a.y += f * v.y;
+                            a.z += f * v.z;
+                            a.w += f * v.w;
+                        }
+                        store(r, c, L, a);
+                    }
                 }
             }
         }
