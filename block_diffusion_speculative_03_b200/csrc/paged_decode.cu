@@ -37,9 +37,11 @@ namespace {
 constexpr int kConsumers = 8;      // two groups of four warps take the tiles in turn
 constexpr int kThreads = 32 + 32 * kConsumers;
 constexpr int kTileKeys = kLineTile;
-constexpr int kOverhead = 2;   // units that starting and joining an item costs, in tiles
-// Smallest share of a CTA, in units (one sequence of 2048, 8 kv heads: 9.7 us with 3; 1.1 more with 2, 1.8
-// more with 6).
+// Units that starting and joining an item costs, in tiles (32 sequences of 1 to 8191, 4 kv heads: 18.4 us
+// with 4 or 6, 18.7 with 3, 19.2 with 2).
+constexpr int kOverhead = 4;
+// Smallest share of a CTA, in units (one sequence of 2048, 8 kv heads: 9.7 us with 3 to 5, 10.8 with 7; a
+// single short item: 5.3 us with 3, 6.4 with 4, 7.1 with 5, 8.9 with 7).
 constexpr int kMinShare = 3;
 
 template <int D> struct DecodeCfg {
