@@ -1,6 +1,7 @@
 // C ABI of libdflash (include/dflash.h): argument validation, workspace and
 // cache layout, tensor-map encoding, and the launch sequence of each call.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <new>
@@ -39,11 +40,16 @@ constexpr int kFoldMaxNT = 16;
 void set_pdl(bool on) { g_pdl = on; }
 bool pdl_enabled() { return g_pdl; }
 void ensure_carveout(const void* fn) {
-    static std::vector<const void*> done;
-    for (const void* f : done)
+    // filled from the front; host threads may meet here (setting the attribute twice does no harm)
+    static std::atomic<const void*> done[256];
+    for (auto& d : done) {
+        const void* f = d.load(std::memory_order_acquire);
         if (f == fn) return;
-    cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared);
-    done.push_back(fn);
+        if (f) continue;
+        cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared);
+        const void* none = nullptr;
+        if (d.compare_exchange_strong(none, fn, std::memory_order_acq_rel) || none == fn) return;
+    }
 }
 
 typedef CUresult (*PFN_encodeTiled_t)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -51,15 +57,14 @@ typedef CUresult (*PFN_encodeTiled_t)(CUtensorMap*, CUtensorMapDataType, cuuint3
                                       CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 static PFN_encodeTiled_t get_encode() {
-    static PFN_encodeTiled_t fn = nullptr;
-    if (!fn) {
+    static const PFN_encodeTiled_t fn = [] {
         void* p = nullptr;
         cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = (PFN_encodeTiled_t)p;
-    }
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                            cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return ok ? (PFN_encodeTiled_t)p : (PFN_encodeTiled_t) nullptr;
+    }();
     return fn;
 }
 

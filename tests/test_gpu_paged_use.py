@@ -1,6 +1,8 @@
 """The paged pool as a program uses it: decode cycles, captured graphs, side streams, strided
 tensors, many entries, large pools, the bridge to the draft cache, and the draft step with a
 sliding window."""
+import threading
+
 import pytest
 import torch
 
@@ -228,6 +230,39 @@ def test_two_pools_on_two_streams():
     for pool, (oa, wa, ob, wb) in zip(pools, want):
         assert pool.status() == 0
         assert torch.equal(oa, wa) and torch.equal(ob[:51], wb[:51])
+
+
+def test_two_pools_from_two_threads():
+    """Host threads with a pool each: the library keeps nothing that they share unguarded."""
+    def work(k, errors):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                pool, model = make_pool(("bf16", "f32")[k], 1, 8, 2, 64, 60, 16, 4, 300, seed=k)
+                seqs = [0, 1, 2]
+                for step in range(25):
+                    counts = [(step * 5 + s * 3) % 9 + 1 for s in seqs]
+                    pool.reserve(i32(counts))
+                    model.reserve(seqs, counts)
+                    q = torch.randn(sum(counts), 8, 64, device="cuda").to(pool.torch_dtype)
+                    start = [0, counts[0], counts[0] + counts[1]]
+                    out = pool.attention(0, q, None, None, i32(start), i32(counts), max(counts))
+                    for s in seqs:
+                        rows = slice(start[s], start[s] + counts[s])
+                        n = model.len[s] + counts[s]
+                        check_rows(out[rows], q[rows], model.rows_of(s, n)[0], model.len[s], n, 64, pool.torch_dtype)
+                    pool.advance(i32(counts))
+                    model.advance(seqs, counts)
+                same(pool, model, k)
+        except BaseException as e:      # noqa: B036 (handed to the test's own thread)
+            errors.append(e)
+
+    errors = []
+    threads = [threading.Thread(target=work, args=(k % 2, errors)) for k in range(4)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not errors, errors
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
