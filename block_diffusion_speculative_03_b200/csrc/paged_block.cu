@@ -394,7 +394,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                     }
                     // V rows that no row sees may hold anything (0 * NaN is NaN): zero them
                     if (k0 + 64 > hi_tile || (k0 < lo_tile && k0 + 64 > p.sinks)) {
-                        mbar_wait_warp(&kv_full[S + it % S], (uint32_t)((it / S) & 1), abort_flag, p.wait_status);
+                        // The softmax may be S tiles and more ahead of the products, and a parity tells two
+                        // phases apart, not three: first the product of the stage's tile before (or of
+                        // a later tile; tile it - 4 is the last whose barrier cannot have gone on
+                        // by another phase), then this tile's V.
+                        constexpr int BACK = S < kBufs - 1 ? S : kBufs - 1;
+                        if (it >= BACK)
+                            mbar_wait_warp(&pv_done[(it - BACK) % kBufs], (uint32_t)(((it - BACK) / kBufs) & 1), abort_flag,
+                                           p.wait_status);
+                        ok = mbar_wait_warp(&kv_full[S + it % S], (uint32_t)((it / S) & 1), abort_flag, p.wait_status);
+                        if (!ok) break;
                         // two threads to a row
                         const int k = k0 + (rl >> 1);
                         if (k >= hi_tile || (k < lo_tile && k >= p.sinks)) {
@@ -484,10 +493,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
                 if (ok) ok = put_q(seg + 1);
             }
             ++seg;
-            {
-                const int last = it0 + s.t1 - s.t0 - 1;
-                if (ok) ok = mbar_wait_warp(&pv_done[last % kBufs], (uint32_t)((last / kBufs) & 1), abort_flag, p.wait_status);
-            }
+            // by the group that had the last tile: it knows that the barrier's phase before is over
+            const int last = it0 + s.t1 - s.t0 - 1;
+            if (ok && !((last ^ w) & 1))
+                ok = mbar_wait_warp(&pv_done[last % kBufs], (uint32_t)((last / kBufs) & 1), abort_flag, p.wait_status);
+            tc_fence_before();
             ml[w * 128 + rl] = make_float2(base, l);
             if (named_bar_or(1, kSoftmax, !ok)) break;
             tc_fence_after();
@@ -496,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             const bool whole = s.whole(), head = s.t0 == 0;   // head: holds the item's first tile
             float* slot = p.partial + (size_t)(2 * blockIdx.x + (head ? 1 : 0)) * kSlot<D>;
             constexpr int HC = D / 2;
-            const float B = base_s[((it0 + s.t1 - s.t0 - 1) & 1) * 128 + rl], z = B == -INFINITY ? 0.f : B;
+            const float B = base_s[(last & 1) * 128 + rl], z = B == -INFINITY ? 0.f : B;
             const float2 m0 = ml[rl], m1 = ml[128 + rl];
             const float L = pow2_int(m0.x - z) * m0.y + pow2_int(m1.x - z) * m1.y;
             if constexpr (CS == 1) {
