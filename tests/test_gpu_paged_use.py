@@ -196,6 +196,35 @@ def test_wide_forks_write_at_once(n, left_out):
     same(pool, model, "advance")
 
 
+@pytest.mark.parametrize("rows,window,page,d", [(16, 4096, 64, 128), (16, 300, 16, 64), (1, 0, 64, 128),
+                                                (60, 500, 64, 128), (9, 0, 32, 64)])
+def test_many_calls_with_a_cold_cache(rows, window, page, d):
+    """The same call hundreds of times, its keys in the L2 cache or flushed from it: loads that come
+    early or late change nothing."""
+    pool, _ = make_pool("bf16", 1, 16, 4, d, 4 * 8300 // page, page, 4, 8300)
+    lens = [8192, 8000, 100, 5001]
+    pool.reserve(i32([n + rows for n in lens]))
+    pool.advance(i32(lens))
+    torch.manual_seed(rows)
+    q = torch.randn(4 * rows, 16, d, device="cuda").bfloat16()
+    args = (i32([0, 1, 2, 3]), i32([0, rows, 2 * rows, 3 * rows]), i32([rows] * 4), rows, rows == 1)
+    flush = torch.empty(40 << 20, dtype=torch.int32, device="cuda")
+    want = pool.attention(0, q, None, *args, window, 16).clone()
+    slab = pool.slab()
+    for s, n in enumerate(lens):
+        pages = pool.table[s, :M.ceil_div(n + rows, page)].long()
+        kv = slab[pages, 0].permute(1, 2, 0, 3, 4).flatten(2, 3)[:, :, :n + rows]
+        mine = slice(s * rows, (s + 1) * rows)
+        check_rows(want[mine], q[mine], kv, n, n + rows, d, torch.bfloat16, rows == 1, window, 16)
+    out, off = torch.empty_like(want), torch.zeros((), dtype=torch.int64, device="cuda")
+    for k in range(600):
+        if k % 5 == 0:
+            flush.fill_(k)
+        pool.attention(0, q, out, *args, window, 16)
+        off += (out.view(torch.int16) != want.view(torch.int16)).sum()
+    assert off.item() == 0 and pool.status() == 0
+
+
 def test_two_pools_on_two_streams():
     """Calls of different pools at once: tokens, blocks and page operations beside one another."""
     torch.manual_seed(5)
