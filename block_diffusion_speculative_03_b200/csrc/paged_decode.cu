@@ -257,7 +257,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
                 }
             }
             const float za = base_a == -INFINITY ? 0.f : base_a, zb = base_b == -INFINITY ? 0.f : base_b;
-            uint32_t pf[4];
+            // P in two terms, bf16(P) and bf16(P - bf16(P)): 16 bits of it
+            uint32_t pf[4], pl[4];
+            auto rest = [](float x, float y, uint32_t hi) {
+                return pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+            };
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const float p0 = ex2_fast(fmaf(sc[j][0], p.scale_log2, -za)), p1 = ex2_fast(fmaf(sc[j][1], p.scale_log2, -za));
@@ -266,6 +270,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
                 l_b += p2 + p3;
                 pf[j * 2] = pack_bf16(p0, p1);
                 pf[j * 2 + 1] = pack_bf16(p2, p3);
+                pl[j * 2] = rest(p0, p1, pf[j * 2]);
+                pl[j * 2 + 1] = rest(p2, p3, pf[j * 2 + 1]);
             }
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
@@ -273,6 +279,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
                 ldsm4t(sv + v_off + (j >> 2) * half + ((((j & 3) * 2 + vc8) ^ (vk & 7)) << 4), b);
                 mma16816(o[2 * j], pf, b[0], b[1]);
                 mma16816(o[2 * j + 1], pf, b[2], b[3]);
+                mma16816(o[2 * j], pl, b[0], b[1]);
+                mma16816(o[2 * j + 1], pl, b[2], b[3]);
             }
             // The arrive goes to an address that a load behind this warp's reads of V returns: the
             // compiler may leave products, and so the wait for what they read, for after it, and without
