@@ -350,8 +350,8 @@ int launch_paged_attn_f32(PagedAttnParams& p, int d, int num_sms, cudaStream_t s
     return d == 128 ? launch_d<128>(p, num_sms, st) : launch_d<64>(p, num_sms, st);
 }
 // Up to 16 vectors fit one register tile.  At 16 (16 rows of 8 heads of 128), this side and the other:
-// 1 sequence of 2000: 14.6 us, 13.3; 4 of 8000: 31.4, 33.3; 32 of 4000: 88.2, 97.4.  At 4: 9.9, 13.2;
-// 27.6, 33.5; 85.4, 95.9.
+// 1 sequence of 2000: 14.7 us, 13.3; 4 of 8000: 30.8, 33.3; 32 of 4000: 89.2, 97.4.  At 4: 10.1, 13.2;
+// 27.5, 33.5; 86.6, 95.9.
 int launch_paged_attn_bf16(PagedAttnParams& p, int d, int num_sms, cudaStream_t st) {
     return p.max_rows * p.G <= 16 ? launch_paged_decode(p, d, num_sms, st) : launch_paged_block(p, d, num_sms, st);
 }

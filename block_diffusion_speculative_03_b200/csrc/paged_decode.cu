@@ -3,7 +3,9 @@
 // joined.
 //
 // With t_k = q.k log2(e) / sqrt(d), out = sum_k P_k v_k / sum_k 2^(t_k - b), P_k =
-// bf16(2^(t_k - b)) for an integer b per row.  b follows the running maximum (kBaseLag,
+// 2^(t_k - b) in two bf16 terms, for an integer b per row.  (One term costs 2^-9 of each weight:
+// 0.0025 off in all, against 0.0017 for rounding the output alone; the second term's products
+// fit beside the loads: 4 x 32768 keys take the same time, one of 2048 0.4 us more.)  b follows the running maximum (kBaseLag,
 // kBaseLead): moving b scales everything by an exact power of two, so the split points
 // and the order of the keys change no rounding of P.
 //
@@ -17,14 +19,14 @@
 //              Boxes in which no row sees a key are not loaded.
 //   warps 1-8  two groups of four that take the tiles in turn, 16 keys of a tile per warp, with
 //              their own running state: S = Q K^T and
-//              O += P V on m16n8k16 tensor instructions, P staying in registers (the
+//              O += P V on m16n8k16 tensor instructions, P's terms staying in registers (the
 //              accumulator layout of S is the operand layout of P).  No barrier between
 //              the warps until the end of the item.  (At 16 rows the tensor work is 1/8 of
 //              what the loads leave time for, so the register path wins over tensor memory:
 //              no hand-offs between issuing, softmax and correction.)
 //
-// Measured, one token, 32 heads on 8 of 128: 4 sequences of 32768 84.2 us (537 MB, 6.4 TB/s, 99 % of
-// a copy); one of 2048 9.7 us, of which 1.3 are HBM: the launch, the dependent reads of the plan
+// Measured, one token, 32 heads on 8 of 128: 4 sequences of 32768 84.0 us (537 MB, 6.4 TB/s, 99 % of
+// a copy); one of 2048 10.2 us, of which 1.3 are HBM: the launch, the dependent reads of the plan
 // (list, length, table), the first load, and the join of 3-tile shares make up the rest.
 #include <algorithm>
 

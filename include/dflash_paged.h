@@ -169,7 +169,8 @@ int dflash_pages_load(dflash_pool* p, const int32_t* seqs, dflash_cache* c, cons
  * With t_k = q.k log2(e) / sqrt(head_dim),
  *   out = R( sum_k P_k v_k / sum_k 2^(t_k - b) ),  P_k = 2^(t_k - b),
  * for an integer b; bf16 pools round P_k to bf16 before it weights v (as
- * dflash_draft_block), fp32 pools do not round it.
+ * dflash_draft_block) in calls with max_rows * n_q_heads / n_kv_heads > 16, and
+ * keep 16 bits of it (two bf16 terms) in smaller ones; fp32 pools do not round it.
  * The keys of an entry may be split over the device in a way that depends on the
  * whole call, so a row's result can differ in its last bits when other entries
  * do; the same call gives the same bits every time.
