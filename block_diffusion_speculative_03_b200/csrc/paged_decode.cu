@@ -25,8 +25,8 @@
 //              what the loads leave time for, so the register path wins over tensor memory:
 //              no hand-offs between issuing, softmax and correction.)
 //
-// Measured, one token, 32 heads on 8 of 128: 4 sequences of 32768 84.0 us (537 MB, 6.4 TB/s, 99 % of
-// a copy); one of 2048 10.2 us, of which 1.3 are HBM: the launch, the dependent reads of the plan
+// Measured, one token, 32 heads on 8 of 128: 4 sequences of 32768 84.9 us (537 MB, 6.3 TB/s, 98 % of
+// a copy); one of 2048 10.1 us, of which 1.3 are HBM: the launch, the dependent reads of the plan
 // (list, length, table), the first load, and the join of 3-tile shares make up the rest.
 #include <algorithm>
 
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
     uint8_t* line_mem = (uint8_t*)(join_ml + kConsumers * 16);
     uint64_t* full = (uint64_t*)(line_mem + kLineBytes);
     uint64_t* empty = full + S;
-    __shared__ int abort_s, flag_s, zero_s;
+    __shared__ int abort_s, flag_s;
     __shared__ long long sums[kThreads / 32];
     volatile int* abort_flag = &abort_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -99,7 +99,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
             mbar_init(&empty[i], kConsumers / 2);
         }
         abort_s = 0;
-        zero_s = 0;
         fence_mbar_init();
         tma_prefetch_desc(&p.tmap);
     }
@@ -232,7 +231,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
                             *reinterpret_cast<uint4*>(vr + h * half + ((lane & 1) * 4 + c) * 16) = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async();      // before the slot's next TMA load
                 }
                 __syncwarp();
             }
@@ -284,13 +282,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
                 mma16816(o[2 * j], pl, b[0], b[1]);
                 mma16816(o[2 * j + 1], pl, b[2], b[3]);
             }
-            // The arrive goes to an address that a load behind this warp's reads of V returns: the
-            // compiler may leave products, and so the wait for what they read, for after it, and without
-            // this the next tile overtook a read now and then (one in 10^10: in 14 of 250000
-            // calls on 4 x 32768 keys some elements were off in their last bits; in none of 250000 with it).
-            const int zero = *(volatile int*)&zero_s;
+            // The reads of V come before the next tile's copy (another proxy): without the fence the compiler
+            // may leave one for after the arrive, and where the loop ends and new code has to be fetched
+            // the copy overtook it (10^-10 of all reads: 14 of 250000 calls on 4 x 32768 keys were off
+            // in their last bits).
+            fence_proxy_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[st + zero]);
+            if (lane == 0) mbar_arrive(&empty[st]);
         }
         // ---- join the warps
         l_a += __shfl_xor_sync(0xffffffffu, l_a, 1);
