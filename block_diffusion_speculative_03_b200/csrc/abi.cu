@@ -1284,6 +1284,10 @@ int dflash_accept(dflash_handle* h, dflash_cache* cc, const int32_t* drafts, con
 // ---------------------------------------------------------------------------
 const char* dflash_diag_arch(void) { return "sm_100a"; }
 
+int dflash_diag_paged_decode_join(int head_dim, int rows, int* room) {
+    return room && paged_decode_join_room(head_dim, rows, room) ? DFLASH_OK : DFLASH_INVALID_ARG;
+}
+
 int dflash_diag_partition(int64_t units, int kb, int ctas, int64_t tile, int* first_cta, int* n_contrib) {
     if (units <= 0 || kb <= 0 || units % kb || ctas <= 0 || ctas > units || tile < 0 || tile * kb >= units || !first_cta ||
         !n_contrib)

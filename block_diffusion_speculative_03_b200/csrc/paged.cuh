@@ -533,6 +533,9 @@ constexpr size_t kJoinRecords = 2048;   // in them: 32 bytes per CTA, what paged
 
 // At most 16 query rows per kv head (paged_decode.cu).
 int launch_paged_decode(PagedAttnParams& p, int d, int num_sms, cudaStream_t st);
+// What its joins of `rows` query rows per kv head write to shared memory, and the room for it: (base,
+// sum) pairs, their room, floats of O, their room.  False: no such shape.
+bool paged_decode_join_room(int d, int rows, int* room);
 // Any number of rows (paged_block.cu).
 int launch_paged_block(PagedAttnParams& p, int d, int num_sms, cudaStream_t st);
 int launch_paged_attn_f32(PagedAttnParams& p, int d, int num_sms, cudaStream_t st);

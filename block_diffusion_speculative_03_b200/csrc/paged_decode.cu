@@ -52,9 +52,18 @@ template <int D> struct DecodeCfg {
     static constexpr int RING = STAGES * 2 * TILE;
     static constexpr int OLD = D + 4;                        // row stride of the join buffer (floats)
     static constexpr int JOIN = kConsumers * 16 * OLD * 4;
-    static constexpr int SMEM = 1024 + RING + JOIN + kConsumers * 16 * 8 + kLineBytes + 256;
+    // (base, sum) pairs: a warp's 16 rows each, or one for every consumer thread (a long join's teams)
+    static constexpr int PAIRS = kConsumers * 32;
+    // offsets from the aligned start: ring, join buffer, pairs, plan, barriers
+    static constexpr int JOIN_AT = RING, PAIRS_AT = JOIN_AT + JOIN, LINE_AT = PAIRS_AT + PAIRS * 8;
+    static constexpr int BARS_AT = LINE_AT + kLineBytes, SMEM = 1024 + BARS_AT + 256;
     static constexpr int SLOT = 16 * (D + 2);                // floats of a partial
+    static_assert(LINE_AT - PAIRS_AT >= kConsumers * 32 * 8 && JOIN >= kConsumers * 32 * 16,
+                  "a long join keeps a pair and four columns of every consumer thread");
+    static_assert(2 * STAGES * 8 <= 256 && SMEM <= 227 * 1024, "shared memory");
 };
+// Teams of E = rows * D / 4 threads that share a long join.
+__host__ __device__ constexpr int join_teams(int E) { return kConsumers * 32 / E < 8 ? kConsumers * 32 / E : 8; }
 
 DF_DEV void ldsm4(uint32_t a, uint32_t* r) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -84,10 +93,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
     constexpr int S = C::STAGES, NT8 = D / 8;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = smem_align_up<uint8_t>(smem_raw, 1024);
-    float* join = (float*)(ring + C::RING);                          // [kConsumers][16][OLD]
-    float2* join_ml = (float2*)(ring + C::RING + C::JOIN);           // [kConsumers][16]
-    uint8_t* line_mem = (uint8_t*)(join_ml + kConsumers * 16);
-    uint64_t* full = (uint64_t*)(line_mem + kLineBytes);
+    float* join = (float*)(ring + C::JOIN_AT);                       // [kConsumers][16][OLD]; long join: [threads][4]
+    float2* join_ml = (float2*)(ring + C::PAIRS_AT);                 // [kConsumers][16]; long join: [threads]
+    uint8_t* line_mem = ring + C::LINE_AT;
+    uint64_t* full = (uint64_t*)(ring + C::BARS_AT);
     uint64_t* empty = full + S;
     __shared__ int abort_s, flag_s;
     __shared__ long long sums[kThreads / 32];
@@ -389,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
                                          ((size_t)(e.y + v) * p.nq + (size_t)s.g * p.G + r - v * p.G) * D + c;
                     *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
                 };
-                const int E = R * (D / 4), teams = min(8, kConsumers * 32 / E);
+                const int E = R * (D / 4), teams = join_teams(E);
                 if (c1 - c0 < 8 || teams < 2) {
                     for (int x = c_tid; x < E; x += kConsumers * 32) {
                         float B = -INFINITY, L = 0.f;
@@ -445,7 +454,22 @@ int launch_d(const PagedAttnParams& p, int num_sms, cudaStream_t st) {
     return (int)launch_k(kern, dim3(std::min(num_sms, kPagedCtas)), dim3(kThreads), DecodeCfg<D>::SMEM, st, p);
 }
 
+template <int D> void join_room(int rows, int* room) {
+    using C = DecodeCfg<D>;
+    const int E = rows * (D / 4), threads = join_teams(E) * E;
+    room[0] = std::max(kConsumers * 16, threads);
+    room[1] = (C::LINE_AT - C::PAIRS_AT) / 8;
+    room[2] = std::max(((kConsumers - 1) * 16 + rows) * C::OLD, threads * 4);
+    room[3] = (C::PAIRS_AT - C::JOIN_AT) / 4;
+}
+
 }  // namespace
+
+bool paged_decode_join_room(int d, int rows, int* room) {
+    if ((d != 64 && d != 128) || rows < 1 || rows > 16) return false;
+    d == 128 ? join_room<128>(rows, room) : join_room<64>(rows, room);
+    return true;
+}
 
 int launch_paged_decode(PagedAttnParams& p, int d, int num_sms, cudaStream_t st) {
     p.rt = p.max_rows;

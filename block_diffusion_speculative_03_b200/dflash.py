@@ -127,6 +127,7 @@ def lib():
         "dflash_diag_gemm_max_active_clusters": (i32, [i32]),
         "dflash_diag_set_norm_fold": (i32, [i32]),
         "dflash_diag_set_inject_partition": (i32, [i32]),
+        "dflash_diag_paged_decode_join": (i32, [i32, i32, C.POINTER(i32)]),
         "dflash_diag_set_o_beside_attention": (i32, [i32]),
         "dflash_diag_wait_selftest": (i32, [vp, vp, vp]),
         "dflash_diag_attention": (i32, [vp, vp, vp, vp, i32, i32, vp]),
@@ -183,7 +184,7 @@ def exported_symbols() -> list:
             "dflash_diag_set_gemm_pre_stages", "dflash_diag_set_split_finisher", "dflash_diag_set_gemm_max_cluster",
             "dflash_diag_set_o_late_deficit", "dflash_diag_set_gemm_tail",
             "dflash_diag_gemm_max_active_clusters",
-            "dflash_diag_set_norm_fold", "dflash_diag_set_inject_partition",
+            "dflash_diag_set_norm_fold", "dflash_diag_set_inject_partition", "dflash_diag_paged_decode_join",
             "dflash_diag_set_o_beside_attention",
             "dflash_diag_wait_selftest",
             "dflash_diag_attention", "dflash_diag_gemm_bf16_traced",
@@ -330,6 +331,13 @@ def dflash_diag_gemm_bf16_noalloc_status(stream: int = 0) -> int:
     v = C.c_int32(0)
     _chk(lib().dflash_diag_gemm_bf16_noalloc_status(C.byref(v), stream), "dflash_diag_gemm_bf16_noalloc_status")
     return v.value
+
+
+def dflash_diag_paged_decode_join(head_dim: int, rows: int):
+    """(pairs written, pairs that fit, floats written, floats that fit)."""
+    room = (C.c_int * 4)()
+    _chk(lib().dflash_diag_paged_decode_join(head_dim, rows, room), "dflash_diag_paged_decode_join")
+    return tuple(room)
 
 
 def dflash_diag_partition(units: int, kb: int, ctas: int, tile: int):

@@ -268,6 +268,11 @@ int dflash_diag_set_o_beside_attention(int on);
  * split-K slabs (its few rows per call stream the weights on every SM). */
 int dflash_diag_set_inject_partition(int whole_tiles);
 
+/* Shared memory of the joins in the attention of few rows over pages (head_dim 64 or
+ * 128, 1..16 query rows per kv head): room = {(base, sum) pairs written, pairs that
+ * fit, floats of O written, floats that fit}.  Host arithmetic only. */
+int dflash_diag_paged_decode_join(int head_dim, int rows, int* room);
+
 /* "sm_100a" for this build. */
 const char* dflash_diag_arch(void);
 

@@ -1,0 +1,52 @@
+"""Long joins of the paged attention of few rows while other work holds the device: whichever share
+of an item arrives last, the ones that go on with the next item read their own plan."""
+import pytest
+import torch
+
+from tests import paged_model as M
+from tests.test_gpu_paged import i32, make_pool
+from tests.test_paged_plan_cpu import LONG
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("nq,nkv,d,lens", LONG)
+def test_long_joins_beside_other_work(nq, nkv, d, lens):
+    page, n = 64, len(lens)
+    pool, _ = make_pool("bf16", 1, nq, nkv, d, sum(M.ceil_div(x + 1, page) for x in lens), page, n, max(lens) + 1)
+    pool.reserve(i32([x + 1 for x in lens]))
+    pool.advance(i32(lens))
+    torch.manual_seed(len(lens) + d)
+    q = torch.randn(n, nq, d, device="cuda").bfloat16()
+    want = pool.attention(0, q).clone()
+    slab = pool.slab()
+    for s, x in enumerate(lens):
+        kv = slab[pool.table[s, :M.ceil_div(x + 1, page)].long(), 0].permute(1, 2, 0, 3, 4).flatten(2, 3)[:, :, :x + 1]
+        ref, mean, score = M.attention(q[s:s + 1], kv[0], kv[1], [x], True, 0, 0)
+        tol = M.bound(ref, mean, score, x + 1, d, torch.bfloat16)
+        assert ((want[s:s + 1].double() - ref).abs() <= tol).all()
+
+    # another pool's blocks and tokens on another stream take the SMs away from some shares for a while
+    other, _ = make_pool("bf16", 1, 16, 4, 128, 300, 64, 4, 4200, seed=1)
+    other.reserve(i32([4100, 3000, 900, 64]))
+    other.advance(i32([4080, 2980, 880, 40]))
+    start, count = i32([0, 16, 32, 48]), i32([16] * 4)
+    qb = torch.randn(64, 16, 128, device="cuda").bfloat16()
+    ob = torch.empty_like(qb)
+    beside = torch.cuda.Stream()
+    beside.wait_stream(torch.cuda.current_stream())
+    out, off = torch.empty_like(want), torch.zeros((), dtype=torch.int64, device="cuda")
+    for k in range(200):
+        with torch.cuda.stream(beside):
+            other.attention(0, qb, ob, None, start, count, 16)
+            if k % 3 == 0:
+                other.attention(0, qb[:4], ob[:4])
+        out.fill_(7.0)
+        pool.attention(0, q, out)
+        off += (out.view(torch.int16) != want.view(torch.int16)).sum()
+    torch.cuda.synchronize()
+    assert off.item() == 0
+    # and the counts of arrivals are as a call finds them: alone again, the same bits
+    out.fill_(7.0)
+    assert torch.equal(pool.attention(0, q, out), want)
+    assert pool.status() == 0 and other.status() == 0
