@@ -5,7 +5,7 @@ import torch
 
 from tests import paged_model as M
 from tests.test_gpu_paged import i32, make_pool
-from tests.test_paged_plan_cpu import LONG
+from tests.test_paged_plan_cpu import LONG, end_holders
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +50,38 @@ def test_long_joins_beside_other_work(nq, nkv, d, lens):
     out.fill_(7.0)
     assert torch.equal(pool.attention(0, q, out), want)
     assert pool.status() == 0 and other.status() == 0
+
+
+@pytest.mark.parametrize("nq,nkv,d,lens", LONG)
+def test_last_to_arrive_goes_on_with_the_next_item(nq, nkv, d, lens):
+    """Single shares that start late.  Blocks start in order, so work that holds k SMs when a call
+    starts makes the last k of its shares late: with k chosen so that the first of them holds the end of
+    an item and the start of the next, that one is the last of its item to arrive, and goes on."""
+    page, n = 64, len(lens)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    pool, _ = make_pool("bf16", 1, nq, nkv, d, sum(M.ceil_div(x + 1, page) for x in lens), page, n, max(lens) + 1)
+    pool.reserve(i32([x + 1 for x in lens]))
+    pool.advance(i32(lens))
+    torch.manual_seed(len(lens) + d)
+    q = torch.randn(n, nq, d, device="cuda").bfloat16()
+    want = pool.attention(0, q).clone()
+    # a softmax over k long rows holds k SMs, a block of 1024 threads on each
+    rows = torch.randn(sms, 200000, device="cuda")
+    held = torch.empty_like(rows)
+    out = torch.empty_like(want)
+    beside = torch.cuda.Stream()
+    for _, left, share in end_holders(lens, nkv, sms):
+        k = sms - share
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            beside.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(beside):
+                torch.softmax(rows[:k], 1, out=held[:k])
+            out.fill_(7.0)
+            pool.attention(0, q, out)
+            torch.cuda.current_stream().wait_stream(beside)
+        for _ in range(10):
+            graph.replay()
+            assert torch.equal(out, want), (k, left)
+    assert torch.equal(pool.attention(0, q, out), want)
+    assert pool.status() == 0

@@ -32,7 +32,7 @@ def test_shapes_without_a_join_are_refused(lib):
 
 
 def end_holders(lens, nkv, ctas=148, overhead=4, least=3):
-    """(tiles of a long item's end, tiles of the next item) of the shares that hold both; long: in
+    """(units of a long item's end, tiles of the next item, share) of the shares that hold both; long: in
     nine shares and more."""
     items = [(n + 1 + 63) // 64 + overhead for n in lens for _ in range(nkv)]
     starts = [sum(items[:i]) for i in range(len(items) + 1)]
@@ -45,7 +45,7 @@ def end_holders(lens, nkv, ctas=148, overhead=4, least=3):
         first, last = owner(starts[i] + overhead), owner(starts[i + 1] - 1)
         left = begin[last + 1] - starts[i + 1] - overhead
         if last - first >= 8 and left > 0:
-            out.append((starts[i + 1] - max(begin[last], starts[i]), left))
+            out.append((starts[i + 1] - max(begin[last], starts[i]), left, last))
     return out
 
 
@@ -56,5 +56,5 @@ def test_long_cases_have_shares_that_go_on(nq, nkv, d, lens):
 
 def test_share_by_hand():
     # one sequence of 32769 keys, 8 kv heads: 8 items of 513 + 4 units over 148 shares of 27 or 28
-    assert end_holders([32768], 8)[0] == (14, 9)
+    assert end_holders([32768], 8)[0] == (14, 9, 18)
     assert end_holders([2047], 8) == []                 # shares end where items do
