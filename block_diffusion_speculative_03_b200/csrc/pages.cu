@@ -84,10 +84,11 @@ DF_DEV int entry_seq(const PoolView& v, const int* seqs, int i) {
     return s >= 0 && s < v.max_seqs ? s : -2;
 }
 // Whether entry i's sequence stands earlier in the list (the calling threads share the search).
-DF_DEV bool listed_before(const int* seqs, int i, int s, int first, int step) {
+// partner: the other list of a pair, or null; beside a -1 there a sequence is not listed.
+DF_DEV bool listed_before(const int* seqs, const int* partner, int i, int s, int first, int step) {
     bool d = false;
     if (seqs)
-        for (int j = first; j < i; j += step) d |= seqs[j] == s;
+        for (int j = first; j < i; j += step) d |= seqs[j] == s && !(partner && partner[j] == -1);
     return d;
 }
 
@@ -119,23 +120,22 @@ __global__ void __launch_bounds__(kPlan) k_pages_plan(PoolView v, const int* __r
     owner[t] = kPlan;
     __syncthreads();
     if (t < n) {
-        const int s = entry_seq(v, seqs, t);
+        const int s = FORK && src[t] == -1 ? -1 : entry_seq(v, seqs, t);
         sid[t] = s;
         first[t] = past[t] = 0;
         if (s >= 0) atomicMin(&owner[s], t);
     }
     __syncthreads();
     if (t < n) {
-        int s = sid[t], err = 0;
+        const int s = sid[t];
+        int err = 0;
         if (s == -2) {
             err = DFLASH_INVALID_ARG;
         } else if (s >= 0) {
             if (owner[s] < t) err = DFLASH_INVALID_ARG;
             if (FORK) {
                 const int a = src[t];
-                if (a == -1) {
-                    s = -1;
-                } else if (a < 0 || a >= v.max_seqs) {
+                if (a < 0 || a >= v.max_seqs) {
                     err = DFLASH_INVALID_ARG;
                 } else {
                     for (int j = 0; j < n; ++j)
@@ -359,7 +359,7 @@ __global__ void k_pages_fork(PoolView v, const int* __restrict__ src, const int*
     const int d = entry_seq(v, dst, i), a = src[i];
     if (d == -1 || a == -1) return;
     bool bad = d == -2 || a < 0 || a >= v.max_seqs;
-    bad |= listed_before(dst, i, d, t, blockDim.x);
+    bad |= listed_before(dst, src, i, d, t, blockDim.x);
     for (int j = t; j < n; j += blockDim.x) bad |= src[j] == d;
     if (__syncthreads_or(bad)) {
         if (t == 0) set_error(v.status, DFLASH_INVALID_ARG);
@@ -387,7 +387,7 @@ __global__ void k_pages_free(PoolView v, const int* __restrict__ seqs, const int
     const int i = blockIdx.x, t = threadIdx.x;
     const int s = entry_seq(v, seqs, i);
     if (s == -1) return;
-    bool bad = s == -2 || listed_before(seqs, i, s, t, blockDim.x);
+    bool bad = s == -2 || listed_before(seqs, nullptr, i, s, t, blockDim.x);
     const int k = keep ? keep[i] : 0;
     if (!bad) bad = k < 0 || k > v.len[s];
     if (__syncthreads_or(bad)) {           // len is read before it is written below
@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(256) k_pages_write(PoolView v, const int* __re
     const int start = row_start ? row_start[i] : i, count = row_start ? row_count[i] : 1;
     if (s == -1 || count == 0) return;
     bool bad = s == -2 || count < 0 || count > max_rows || start < 0 || start > total_rows - count;
-    bad |= listed_before(seqs, i, s, t, blockDim.x);
+    bad |= listed_before(seqs, nullptr, i, s, t, blockDim.x);
     if (__syncthreads_or(bad)) {
         if (t == 0) set_error(v.status, DFLASH_INVALID_ARG);
         return;
@@ -650,7 +650,7 @@ __global__ void k_exchange_plan(PoolView v, const int* __restrict__ seqs, SlabVi
     if (t == 0) v.recs[i] = make_int4(s, b, 0, 0);
     if (s == -1 || b == -1) return;
     bool bad = s == -2 || b < 0 || b >= c.batch;
-    bad |= load ? listed_before(reqs, i, b, t, blockDim.x) : listed_before(seqs, i, s, t, blockDim.x);
+    bad |= load ? listed_before(reqs, seqs, i, b, t, blockDim.x) : listed_before(seqs, reqs, i, s, t, blockDim.x);
     if (__syncthreads_or(bad)) {
         if (t == 0) set_error(v.status, DFLASH_INVALID_ARG);
         return;

@@ -111,9 +111,10 @@ int dflash_pages_reserve(dflash_pool* p, const int32_t* seqs, const int32_t* gro
 /* dst[i] becomes src[i]'s context: the same pages up to ceil(len / page_size)
  * (deep == 0), or copies of them in free pages (deep != 0; taken as in reserve,
  * CAPACITY and nothing changed when they do not suffice).  src and dst: device
- * int32[n]; a pair with src or dst -1 is padding.  A source may occur any number
- * of times.  A destination must be empty (len 0 and no pages: STATE otherwise),
- * occur once, and not be a source of the same call (INVALID_ARG). */
+ * int32[n]; a pair with src or dst -1 is padding: what stands beside the -1 is not
+ * looked at, except that no destination may stand in src, beside a dst of -1 either.
+ * A source may occur any number of times.  A destination must be empty (len 0 and no
+ * pages: STATE otherwise), occur once, and not stand in src (INVALID_ARG). */
 int dflash_pages_fork(dflash_pool* p, const int32_t* src, const int32_t* dst, int n, int deep, dflash_stream stream);
 
 /* Cut each listed sequence back to keep[i] positions (device int32[n], NULL = 0:
@@ -148,7 +149,8 @@ int dflash_pages_advance(dflash_pool* p, const int32_t* seqs, const int32_t* row
  * 0..n-1; the cache's shape and type must match the pool's) and set the sequence's
  * len.  The positions must be reserved (CAPACITY, STATE as in write).  Nothing is
  * done where the sequence is at least as long.  The caller vouches that both hold
- * the same context up to the shorter length. */
+ * the same context up to the shorter length.  A pair with seqs or reqs -1 is padding:
+ * what stands beside the -1 is not looked at (here and in dflash_pages_load). */
 int dflash_pages_store(dflash_pool* p, const int32_t* seqs, const dflash_cache* c, const int32_t* reqs, int n,
                        dflash_stream stream);
 

@@ -1,0 +1,111 @@
+"""Calls at the edge of what the paged pool's documents allow: padding beside stale ids, refused
+entries among good ones, windows as long as an int holds."""
+import random
+
+import pytest
+import torch
+
+from block_diffusion_speculative_03_b200 import inputs as I
+from tests import paged_model as M
+from tests.test_gpu_paged import i32, make_pool, same
+from tests.test_gpu_paged_use import drafter
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------
+# Padding
+# ---------------------------------------------------------------------------
+
+def model_fork(model, src, dst, deep):
+    """The model's fork of the pairs that are no padding."""
+    pairs = [(a, b) for a, b in zip(src, dst) if a != -1 and b != -1]
+    model.fork([a for a, _ in pairs], [b for _, b in pairs], deep)
+
+
+@pytest.mark.parametrize("deep", [False, True])
+@pytest.mark.parametrize("src,dst", [
+    ([-1, 0], [5, 5]),                 # the destination stands beside a padding source first
+    ([-1, -1, 0, 1], [5, 4, 4, 5]),
+    ([-1, 0], [99, 5]), ([-1, 0], [-7, 5]),        # .. or an id that does not exist does
+    ([99, 0], [-1, 5]), ([-7, 0], [-1, 5]),
+    ([0, 0], [-1, 5]), ([-1, -1], [-1, -1]), ([-1, 0, 0], [0, 5, 4]),
+])
+def test_padding_pairs_of_a_fork(deep, src, dst):
+    pool, model = make_pool(seqs=6)
+    pool.reserve(i32([20, 37]), i32([0, 1]))
+    pool.advance(i32([20, 37]), i32([0, 1]))
+    model.reserve([0, 1], [20, 37])
+    model.advance([0, 1], [20, 37])
+    pool.fork(i32(src), i32(dst), deep=deep)
+    model_fork(model, src, dst, deep)
+    assert not model.err
+    same(pool, model, (src, dst))
+
+
+@pytest.mark.parametrize("deep", [False, True])
+def test_a_destination_in_src_is_refused_beside_padding_too(deep):
+    pool, model = make_pool(seqs=6)
+    pool.reserve(i32([20]), i32([0]))
+    pool.advance(i32([20]), i32([0]))
+    model.reserve([0], [20])
+    model.advance([0], [20])
+    pool.fork(i32([0, 5]), i32([5, -1]), deep=deep)
+    model.err = {-1}
+    same(pool, model, "refused")
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_random_forks_with_padding_on_either_side(seed):
+    r = random.Random(seed)
+    seqs, page = 12, 16
+    pool, model = make_pool(pages=90, page=page, seqs=seqs, max_len=90, seed=seed)
+    for step in range(60):
+        n = r.randint(1, seqs)
+        dst = [r.choice([-1, seqs, s, r.randrange(seqs)]) if r.random() < 0.4 else s for s in r.sample(range(seqs), n)]
+        src = []
+        for b in dst:
+            a = r.choice([-1, -1, seqs + 3, -2, r.randrange(seqs)]) if r.random() < 0.5 else r.randrange(seqs)
+            src.append(-1 if b == -1 and a in dst else a)      # (no destination beside a dst of -1)
+        deep = r.random() < 0.5
+        pool.fork(i32(src), i32(dst), deep=deep)
+        model_fork(model, src, dst, deep)
+        same(pool, model, (step, src, dst, deep))
+        ids = r.sample(range(seqs), 4)
+        pool.free(i32(ids))
+        model.free(ids)
+        grow = [r.choice([0, 3, 17, 33]) for _ in ids[:2]]
+        pool.reserve(i32(grow), i32(ids[:2]))
+        model.reserve(ids[:2], grow)
+        same(pool, model, (step, "reserve"))
+        if not model.err:
+            pool.advance(i32(grow), i32(ids[:2]))
+            model.advance(ids[:2], grow)
+            same(pool, model, (step, "advance"))
+
+
+def test_padding_pairs_of_store_and_load():
+    w = I.Workload("pad", 256, 2, 4, 2, 64, 512, 1000, 1, 256, 1e6, 1e-6, "bf16", batch=3, gamma=4, context=[1, 1, 1],
+                   mask_id=999, seed=5)
+    dr = drafter(w)
+    cache, back = dr.new_cache(3, 200), dr.new_cache(3, 200)
+    torch.manual_seed(3)
+    for c in (cache, back):
+        c.slab().copy_(torch.randn(c.slab().shape, device="cuda"))
+    cache.set_len(torch.tensor([50, 17, 90], dtype=torch.int32))
+    pool = dr.new_pool(40, 16, 6, 200)
+    pool.reserve(i32([90, 90]), i32([0, 3]))
+    # a sequence beside a padding request, a request beside a padding sequence, ids that do not exist
+    pool.store(cache, i32([0, 0, -1, -1, 77, 3]), i32([-1, 2, 1, 44, -1, 1]))
+    assert pool.status() == 0 and pool.len.tolist() == [90, 0, 0, 17, 0, 0]
+    ids = pool.table[0, :6].long()
+    assert torch.equal(pool.slab()[ids].permute(1, 2, 3, 0, 4, 5).flatten(3, 4)[:, :, :, :90], cache.slab()[2, :, :, :, :90])
+    pool.load(back, i32([-1, 0, 3, 3, -1, 77]), i32([1, 1, -1, 0, 44, -1]))
+    assert pool.status() == 0 and back.len.tolist() == [17, 90, 0] and back.committed.tolist() == [17, 90, 0]
+    assert torch.equal(back.slab()[1, :, :, :, :90], cache.slab()[2, :, :, :, :90])
+    assert torch.equal(back.slab()[0, :, :, :, :17], cache.slab()[1, :, :, :, :17])
+    # the same on both sides is still once only
+    pool.store(cache, i32([1, 1]), i32([0, 0]))
+    assert pool.status() in (-1, -5)
+    pool.load(back, i32([0, 0]), i32([2, 2]))
+    assert pool.status() == -1 and back.len.tolist() == [17, 90, 90]
