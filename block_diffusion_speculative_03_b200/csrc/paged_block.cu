@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_block(const __grid_consta
             const int hi_all = p.causal ? e.w + s.r0 + 1 : hi_tile;    // keys below are seen by all rows ..
             const int lo_all = p.window > 0 ? e.w + s.r1 - p.window : 0;   // .. from here on
             const int hi_row = p.causal ? min(pos + 1, hi_tile) : hi_tile;
-            const int lo_row = p.window > 0 ? pos - p.window + 1 : 0;
+            const int lo_row = p.window > 0 ? max(0, pos - p.window + 1) : 0;   // (less a key's index stays an int)
             float base = -INFINITY, l = 0.f;
             for (int t = s.t0 + ((it0 ^ w) & 1); ok && t < s.t1; t += 2) {
                 const int it = it0 + t - s.t0;

@@ -109,3 +109,28 @@ def test_padding_pairs_of_store_and_load():
     assert pool.status() in (-1, -5)
     pool.load(back, i32([0, 0]), i32([2, 2]))
     assert pool.status() == -1 and back.len.tolist() == [17, 90, 90]
+
+
+# ---------------------------------------------------------------------------
+# Windows that reach past every key
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,nq,nkv,d,rows", [("bf16", 8, 2, 128, 64), ("bf16", 4, 2, 64, 64), ("bf16", 2, 2, 64, 100),
+                                                 ("bf16", 16, 2, 128, 300), ("bf16", 4, 2, 64, 3), ("f32", 4, 2, 64, 64)])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (2 ** 31 - 40, 0), (2 ** 31 - 1, 2 ** 31 - 1), (1 << 30, 5)])
+def test_a_window_longer_than_any_context(dtype, nq, nkv, d, rows, causal, window, sinks):
+    lens = [100, 0, 700]
+    pool, model = make_pool(dtype, 1, nq, nkv, d, 120, 16, 3, 700 + rows)
+    pool.reserve(i32([n + rows for n in lens]))
+    pool.advance(i32(lens))
+    model.reserve([0, 1, 2], [n + rows for n in lens])
+    q = torch.randn(3 * rows, nq, d, device="cuda").to(pool.torch_dtype)
+    out = pool.attention(0, q, None, None, i32([0, rows, 2 * rows]), i32([rows] * 3), rows, causal, window, sinks)
+    assert pool.status() == 0
+    for s, n in enumerate(lens):
+        mine = slice(s * rows, (s + 1) * rows)
+        kv = model.rows_of(s, n + rows)[0]
+        ref, mean, score = M.attention(q[mine], kv[0], kv[1], range(n, n + rows), causal, 0, 0)     # sees all
+        tol = M.bound(ref, mean, score, n + rows, d, pool.torch_dtype)
+        assert ((out[mine].double() - ref).abs() <= tol).all(), s
