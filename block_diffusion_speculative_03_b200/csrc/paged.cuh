@@ -191,7 +191,7 @@ constexpr float kBaseLag = 8.0f, kBaseLead = 8.0f;
 // Shared memory of a CTA: the entries and the units before each.  Units are 32-bit (2^31 of them
 // are two hours of work for a whole device; a call with more records DFLASH_UNSUPPORTED).
 struct Line {
-    int4* ent;          // [n]: sequence, first row, rows (0: nothing to do), length
+    int4* ent;          // [n]: sequence, first row, rows (0: nothing to do), length (-r: r rows to zero)
     int* pre;           // [n + 1]
     int n, rt, ovh, nkv, causal, window, sinks;
 
@@ -206,8 +206,20 @@ struct Line {
 };
 constexpr int kLineBytes = kPoolMaxSeqs * 16 + (kPoolMaxSeqs + 4) * 4;
 
+// Zero the rows of refused entries: the whole device, 16 bytes a thread at a time.
+template <int THREADS, int D> DF_DEV void zero_rows(const PagedAttnParams& p, const Line& L) {
+    for (int i = 0; i < L.n; ++i) {
+        const int4 e = L.ent[i];
+        if (e.z != 0 || e.w >= 0) continue;
+        uint4* o = (uint4*)((__nv_bfloat16*)p.out + (size_t)e.y * p.nq * D);
+        const size_t nz = (size_t)-e.w * p.nq * D / 8;
+        for (size_t x = (size_t)blockIdx.x * THREADS + threadIdx.x; x < nz; x += (size_t)gridDim.x * THREADS)
+            o[x] = make_uint4(0, 0, 0, 0);
+    }
+}
+
 // Fill the line (the whole block; sums: THREADS / 32 long longs of shared memory).  Rows of
-// bad entries are zeroed, each entry by one CTA.  Returns U, 0 when there is nothing to do.
+// bad entries are zeroed.  Returns U, 0 when there is nothing to do.
 template <int THREADS, int D>
 DF_DEV int line_plan(const PagedAttnParams& p, Line& L, uint8_t* mem, long long* sums, int ovh) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -222,16 +234,16 @@ DF_DEV int line_plan(const PagedAttnParams& p, Line& L, uint8_t* mem, long long*
     L.sinks = p.sinks;
     long long w = 0;              // units of entry tid, in the one-row-tile case of the first THREADS entries
     const bool quick = p.n <= 32 && p.row_tiles == 1;      // one warp scans
+    bool refused = false;         // this thread has an entry whose rows are to be zeroed
     for (int i = tid; i < p.n; i += THREADS) {
         AttnEntry e = attn_entry(p, i);
         if (e.bad) {
-            if (i % (int)gridDim.x == (int)blockIdx.x) {
-                if (p.status) set_error(p.status, e.bad);
-                uint4* o = (uint4*)((__nv_bfloat16*)p.out + (size_t)e.start * p.nq * D);
-                const size_t nz = (size_t)e.count * p.nq * D / 8;
-                for (size_t x = 0; x < nz; ++x) o[x] = make_uint4(0, 0, 0, 0);
-            }
+            if (p.status && i % (int)gridDim.x == (int)blockIdx.x) set_error(p.status, e.bad);
+            refused |= e.count > 0;
+            e.len = -e.count;
             e.count = 0;
+        } else if (e.count == 0) {
+            e.len = 0;
         }
         L.ent[i] = make_int4(e.seq, e.start, e.count, e.len);
         if (p.row_tiles == 1) {
@@ -250,14 +262,14 @@ DF_DEV int line_plan(const PagedAttnParams& p, Line& L, uint8_t* mem, long long*
             if (lane < p.n) L.pre[lane] = (int)min(inc - w, 0x7fffffffll);
             if (lane == p.n - 1) sums[0] = inc;
         }
-        __syncthreads();
+        if (__syncthreads_or(refused)) zero_rows<THREADS, D>(p, L);
         const long long all = sums[0];
         if (tid == 0) L.pre[p.n] = (int)min(all, 0x7fffffffll);
         __syncthreads();
         if (all >= 0x7fffffffll && tid == 0 && p.wait_status) set_error(p.wait_status, DFLASH_UNSUPPORTED);
         return all < 0x7fffffffll ? (int)all : 0;
     }
-    __syncthreads();
+    if (__syncthreads_or(refused)) zero_rows<THREADS, D>(p, L);
     if (p.row_tiles > 1) {
         for (int i = warp; i < p.n; i += THREADS / 32) {
             const int4 e = L.ent[i];

@@ -134,3 +134,61 @@ def test_a_window_longer_than_any_context(dtype, nq, nkv, d, rows, causal, windo
         ref, mean, score = M.attention(q[mine], kv[0], kv[1], range(n, n + rows), causal, 0, 0)     # sees all
         tol = M.bound(ref, mean, score, n + rows, d, pool.torch_dtype)
         assert ((out[mine].double() - ref).abs() <= tol).all(), s
+
+
+# ---------------------------------------------------------------------------
+# Refused entries among good ones
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,rows", [(20, 1), (20, 7), (20, 130), (500, 1), (500, 33)])
+def test_refused_entries_are_zeroed_and_the_others_right(dtype, n, rows):
+    """Every third entry without room, every seventh of a sequence that does not exist, some padding:
+    on both sides of 32 entries, with one row tile and several."""
+    nq, nkv, d = 4, 2, 64
+    pool, model = make_pool(dtype, 1, nq, nkv, d, 60, 16, 4, 300)
+    lens = [100, 0, 37, 64]
+    pool.reserve(i32([n + rows for n in lens[:3]] + [64]))
+    pool.advance(i32(lens))
+    model.reserve([0, 1, 2], [n + rows for n in lens[:3]])
+    seqs = [3 if i % 3 == 0 else 4 + i if i % 7 == 0 else -1 if i % 11 == 0 else i % 3 for i in range(n)]
+    total = n * rows + 5
+    q = torch.randn(total, nq, d, device="cuda").to(pool.torch_dtype)
+    out = torch.full_like(q, 7.0)
+    pool.attention(0, q, out, i32(seqs), i32([i * rows for i in range(n)]), i32([rows] * n), rows)
+    assert pool.status() in (-1, -5)
+    assert (out[n * rows:] == 7).all()
+    for i, s in enumerate(seqs):
+        mine = slice(i * rows, (i + 1) * rows)
+        if s == -1:
+            assert (out[mine] == 7).all(), i
+        elif s >= 3:
+            assert (out[mine] == 0).all(), i
+        elif i < 40:
+            kv = model.rows_of(s, lens[s] + rows)[0]
+            ref, mean, score = M.attention(q[mine], kv[0], kv[1], range(lens[s], lens[s] + rows), True, 0, 0)
+            tol = M.bound(ref, mean, score, lens[s] + rows, d, pool.torch_dtype)
+            assert ((out[mine].double() - ref).abs() <= tol).all(), i
+
+
+def test_a_refused_prompt_does_not_hold_up_the_call():
+    """A chunk of 2048 rows without room beside a block: its 16 MB of zeros are written by the whole
+    device (a few microseconds; one thread took milliseconds)."""
+    pool, _ = make_pool("bf16", 1, 32, 8, 128, 40, 64, 2, 2200)
+    pool.reserve(i32([100]), i32([0]))
+    q = torch.randn(2048 + 16, 32, 128, device="cuda").bfloat16()
+    out = torch.empty_like(q)
+    args = (i32([1, 0]), i32([0, 2048]), i32([2048, 16]), 2048)
+    times = []
+    for _ in range(8):
+        out.fill_(7.0)
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        pool.attention(0, q, out, *args)
+        b.record()
+        b.synchronize()
+        times.append(a.elapsed_time(b) * 1e3)
+    assert pool.status() == -5
+    assert (out[:2048] == 0).all() and torch.isfinite(out[2048:].float()).all() and (out[2048:] != 7).any()
+    print(sorted(times))
+    assert min(times) < 300, times
