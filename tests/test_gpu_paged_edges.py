@@ -1,5 +1,6 @@
 """Calls at the edge of what the paged pool's documents allow: padding beside stale ids, refused
 entries among good ones, windows as long as an int holds."""
+import math
 import random
 
 import pytest
@@ -192,3 +193,52 @@ def test_a_refused_prompt_does_not_hold_up_the_call():
     assert (out[:2048] == 0).all() and torch.isfinite(out[2048:].float()).all() and (out[2048:] != 7).any()
     print(sorted(times))
     assert min(times) < 300, times
+
+
+# ---------------------------------------------------------------------------
+# Accuracy of few rows
+# ---------------------------------------------------------------------------
+
+def two_terms_bound(out, mean, score, n, d):
+    """As M.bound for bf16, with weights kept in two bf16 terms: the first is off by half a step, 2^-8 of
+    the weight, what is left (exact in fp32) is rounded by 2^-8 of that: 2^-16."""
+    f32 = 2 * (2 * d * 2.0 ** -23 * score) + 2.0 ** -20 + 2 * n * 2.0 ** -23
+    e = (2.0 ** -16 + f32) * mean
+    return e + 2.0 ** -8 * (out.abs() + e) + 1e-30
+
+
+def one_term(q, k, v):
+    """What one bf16 term gives: o = sum R(2^(t - b)) v / sum 2^(t - b) in 64 bits, b the integer below
+    the row's maximum (rows q [1, nq, d] that see all of k, v [nkv, n, d])."""
+    q, k, v = q.double(), k.double(), v.double()
+    k, v = (x.repeat_interleave(q.shape[1] // x.shape[0], 0) for x in (k, v))
+    t = (k @ q[0, :, :, None])[..., 0] / math.sqrt(q.shape[2]) * math.log2(math.e)
+    w = torch.exp2(t - t.amax(1, keepdim=True).floor())
+    return (((w.float().bfloat16().double()[..., None] * v).sum(1)) / w.sum(1, keepdim=True))[None]
+
+
+@pytest.mark.parametrize("nq,nkv,d,page", [(32, 8, 128, 64), (8, 8, 64, 16), (16, 1, 64, 16), (12, 2, 128, 32)])
+def test_few_rows_keep_16_bits_of_the_weights(nq, nkv, d, page):
+    """Contexts of 1 to 7 positions, scores near 0: weighted sums of few values that nearly cancel, where
+    a weight of 8 bits shows before the result's own rounding does."""
+    lens = [1, 2, 3, 4, 5, 6, 7, 3] * 8
+    pool, model = make_pool("bf16", 1, nq, nkv, d, len(lens), page, len(lens), 16, seed=d)
+    pool.reserve(i32([n + 1 for n in lens]))
+    pool.advance(i32(lens))
+    model.reserve(list(range(len(lens))), [n + 1 for n in lens])
+    g = torch.Generator(device="cuda")
+    g.manual_seed(page)
+    q = (torch.randn(len(lens), nq, d, device="cuda", generator=g) * 0.25).bfloat16()
+    out = pool.attention(0, q)
+    assert pool.status() == 0
+    shows = 0
+    for s, n in enumerate(lens):
+        kv = model.rows_of(s, n + 1)[0]
+        ref, mean, score = M.attention(q[s:s + 1], kv[0], kv[1], [n], True, 0, 0)
+        tol = two_terms_bound(ref, mean, score, n + 1, d)
+        assert ((out[s:s + 1].double() - ref).abs() <= tol).all(), s
+        # the result of one term, rounded or not, is outside in many places
+        one = one_term(q[s:s + 1], kv[0], kv[1])
+        shows += ((one - ref).abs() > tol).sum().item()
+    assert shows > 100
+    print(shows, out.numel())
