@@ -85,3 +85,39 @@ def test_last_to_arrive_goes_on_with_the_next_item(nq, nkv, d, lens):
             assert torch.equal(out, want), (k, left)
     assert torch.equal(pool.attention(0, q, out), want)
     assert pool.status() == 0
+
+
+@pytest.mark.parametrize("dtype,nq,nkv,d,lens,rows,causal,window", [
+    ("bf16", 8, 1, 64, [9000], 1, True, 0), ("bf16", 16, 4, 128, [8000, 40, 5000], 3, False, 0),
+    ("bf16", 32, 8, 128, [8000, 100], 16, False, 2000), ("bf16", 8, 2, 128, [4000, 3000], 8, True, 0),
+    ("bf16", 16, 2, 128, [1500], 300, True, 0), ("f32", 8, 8, 64, [3000], 1, True, 0),
+    ("f32", 4, 2, 128, [2500, 900], 8, False, 500)])
+def test_late_shares_change_no_bits(dtype, nq, nkv, d, lens, rows, causal, window):
+    """Every kernel with its last blocks held up for a while, by many or few: the same bits."""
+    page, n = 64, len(lens)
+    pool, _ = make_pool(dtype, 1, nq, nkv, d, sum(M.ceil_div(x + rows, page) for x in lens), page, n, max(lens) + rows)
+    pool.reserve(i32([x + rows for x in lens]))
+    pool.advance(i32(lens))
+    torch.manual_seed(rows)
+    q = torch.randn(n * rows, nq, d, device="cuda").to(pool.torch_dtype)
+    args = (i32(list(range(n))), i32([i * rows for i in range(n)]), i32([rows] * n), rows, causal, window, 4)
+    want = pool.attention(0, q, None, *args).clone()
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    x = torch.randn(sms, 200000, device="cuda")
+    held, out, beside = torch.empty_like(x), torch.empty_like(want), torch.cuda.Stream()
+    for k in range(3, sms, 8):
+        long = (50000, 200000)[k // 8 % 2]
+        a, b = x[:k, :long].contiguous(), held.view(-1)[:k * long].view(k, long)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            beside.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(beside):
+                torch.softmax(a, 1, out=b)
+            out.fill_(7.0)
+            pool.attention(0, q, out, *args)
+            torch.cuda.current_stream().wait_stream(beside)
+        for _ in range(3):
+            out.fill_(0.0)
+            graph.replay()
+            assert torch.equal(out, want), k
+    assert pool.status() == 0
