@@ -929,7 +929,11 @@ static int layers_bf16(dflash_handle* h, dflash_cache* cc, int gamma, bool inges
     ap.status = h->status;
     ap.causal = ingest ? 1 : 0;
     const int attn_blocks = splits * c.n_kv_heads * B;
-    PagedAttnParams wp;   // the same rows through the windowed attention (dflash_cache_set_window)
+    // The same rows through the windowed attention (dflash_cache_set_window), which joins split items in a
+    // launch of its own.  Qwen3-8B-shaped step, 5 layers, gamma 16, captured: batch 1 at 2048 positions 696 us
+    // without a window, 713 with 256, 710 with 1024, 720 with 2048; at 32768 positions 915 without, 711 with
+    // 1024, 741 with 4096, 846 with all of them; batch 4 at 32768: 1363, 869, 930, 1348.
+    PagedAttnParams wp;
     std::memset(&wp, 0, sizeof(wp));
     if (cc->window > 0) {
         wp.tmap = cc->tm_window;

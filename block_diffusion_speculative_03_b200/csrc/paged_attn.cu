@@ -20,7 +20,10 @@
 // 58 there, but 171 against 124 at 32 of 3000 with head_dim 64, the reads of K from shared memory
 // repeated by each).  Bound by latency at few keys (2 x 4 heads of 64, 300 keys: 9.7 us), by
 // shared-memory reads and fp32 instructions at many (32 sequences of 3000, 8 heads of 64: 393 MB
-// in 70 us, 5.6 TB/s, at one row; 124 us at eight).
+// in 71 us, 5.5 TB/s, at one row; 125 us at eight).  16 sequences of 16000, one row, 8 heads of 128 with a
+// window of 1024: 43 us (135 MB, 3.1 TB/s).  A prompt reads K and V once for every eight vectors: 512
+// rows of 8 heads on 2 of 128 behind 1000 positions take 207 us (13 TFLOP/s), 2048 rows of 32 heads on 8
+// with a window of 2048 4.2 ms (16 TFLOP/s).
 #include <algorithm>
 
 #include "paged.cuh"

@@ -24,8 +24,9 @@
 // partials of 32 KB took one CTA 15 us, all SMs together 2 us.
 //
 // Few rows on long contexts are bound by HBM (32 sequences of 4000 with 8 heads of 128, 8 rows of
-// 4 heads: 97 us for 524 MB, 5.4 TB/s), many rows by the softmax warps: 2048 rows of 32 heads of 128
-// behind 6000 positions with a window of 2048 take 86 us, 0.8 PFLOP/s of products, at 900 cycles a
+// 4 heads: 98 us for 524 MB, 5.4 TB/s), many rows by the softmax warps: 2048 rows of 32 heads of 128
+// behind 6000 positions with a window of 2048 take 86.7 us in a captured graph, 0.79 PFLOP/s of products
+// (96.7 us, 0.71, as calls one after another; without the window 212 us, 1.1 PFLOP/s), at 900 cycles a
 // tile where the tensor cores need 520 and the exponentials 512, and 6000 cycles more for each
 // stretch's end and beginning.  What the time is not: taking out exponentials, conversions or most
 // of the products changed it by less than 1 %; it is the waits and the chain read S - maximum -

@@ -25,9 +25,10 @@
 //              what the loads leave time for, so the register path wins over tensor memory:
 //              no hand-offs between issuing, softmax and correction.)
 //
-// Measured, one token, 32 heads on 8 of 128: 4 sequences of 32768 84.9 us (537 MB, 6.3 TB/s, 98 % of
-// a copy); one of 2048 10.1 us, of which 1.3 are HBM: the launch, the dependent reads of the plan
-// (list, length, table), the first load, and the join of 3-tile shares make up the rest.
+// Measured in a captured graph, one token, 32 heads on 8 of 128: 4 sequences of 32768 85.2 us (537 MB,
+// 6.3 TB/s, 97 % of a copy; 88 us, 94 %, as calls one after another); one of 2048 10.0 us (10.9), of which
+// 1.3 are HBM: the launch, the dependent reads of the plan (list, length, table), the first load, and
+// the join of 3-tile shares make up the rest.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -39,11 +40,11 @@ namespace {
 constexpr int kConsumers = 8;      // two groups of four warps take the tiles in turn
 constexpr int kThreads = 32 + 32 * kConsumers;
 constexpr int kTileKeys = kLineTile;
-// Units that starting and joining an item costs, in tiles (32 sequences of 1 to 8191, 4 kv heads: 18.4 us
-// with 4 or 6, 18.7 with 3, 19.2 with 2).
+// Units that starting and joining an item costs, in tiles (32 sequences of 1 to 8191, 4 kv heads: 18.2 us
+// with 4, 18.8 with 6, 19.0 with 3, 19.2 with 2).
 constexpr int kOverhead = 4;
-// Smallest share of a CTA, in units (one sequence of 2048, 8 kv heads: 9.7 us with 3 to 5, 10.8 with 7; a
-// single short item: 5.3 us with 3, 6.4 with 4, 7.1 with 5, 8.9 with 7).
+// Smallest share of a CTA, in units (one sequence of 2048, 8 kv heads: 9.9 us with 3, 9.3 with 4, 9.7 with
+// 5, 10.3 with 7; one of 512, one head: 7.0, 7.2, 7.9, 7.2).
 constexpr int kMinShare = 3;
 
 template <int D> struct DecodeCfg {
@@ -408,7 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_decode(const __grid_const
                     }
                 } else {
                     // few rows, many partials: teams of threads take eight partials each in turn (one
-                    // sequence of 2048, 8 kv heads of 4 rows, 12 partials: 9.7 us, 10.1 without)
+                    // sequence of 32768, one kv head, 4 rows, 148 partials: 26.4 us, 43.2 without; one row:
+                    // 14.5, 44.0; of 2048, 8 kv heads of 4 rows, 12 partials: 9.9, 10.0)
                     const int team = c_tid / E, x = c_tid - team * E, r = x / (D / 4), c = (x % (D / 4)) * 4;
                     float B = -INFINITY, L = 0.f;
                     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);

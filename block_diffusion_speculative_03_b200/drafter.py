@@ -68,7 +68,9 @@ class Cache:
 
     def set_window(self, window: int, sinks: int = 0) -> None:
         """From now on draft_block (and ingest_fused_input) on this cache see only the last
-        `window` positions and the first `sinks` of the context; 0 turns the window off."""
+        `window` positions and the first `sinks` of the context; 0 turns the window off.
+        A step at long contexts gets shorter with it (915 to 711 us at 32768 positions with a
+        window of 1024), one at 2048 positions does not (1 % shorter to 4 % longer)."""
         if window > 0 and self._window_buf is None:
             self._window_bytes = D.dflash_window_scratch_bytes()
             self._window_buf, self._window_ptr = _aligned_empty(self._window_bytes, self.drafter.device)

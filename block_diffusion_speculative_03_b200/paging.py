@@ -4,6 +4,8 @@
 layer's keys and values, handed out to sequences through tables on the device.  Its methods
 carry the C calls' meaning; they check shapes, types and devices, pass pointers and the
 current CUDA stream of the pool's device, and never synchronise (except :meth:`status`).
+The pool's memory belongs to the stream it was made on: before a pool that was used on another
+one is dropped, that stream's work has to be done (or waited for).
 
     pool = drafter.new_pool(n_pages=4096, page_size=64, max_seqs=64, max_len=32768)
     pool.reserve(grow)                          # room for the rows about to be written
@@ -133,7 +135,7 @@ class PagePool:
         self._run(self._lib.dflash_pages_reserve, a, g, n)
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor, deep: bool = False) -> None:
-        """dst[i] shares src[i]'s pages (deep: gets copies of them)."""
+        """dst[i] shares src[i]'s pages (deep: gets copies of them).  A pair with a -1 is padding."""
         n = src.numel()
         a, b = self._ids(src, "src"), self._ids(dst, "dst", n)
         self._run(self._lib.dflash_pages_fork, a, b, n, 1 if deep else 0)

@@ -179,14 +179,17 @@ int dflash_pages_load(dflash_pool* p, const int32_t* seqs, dflash_cache* c, cons
  * q: device, storage type, row r at q + r * q_stride elements (>= n_q_heads *
  * head_dim, rows 16-byte aligned), a row is [n_q_heads][head_dim].  out: device
  * [total_rows][n_q_heads][head_dim], 16-byte aligned, no part of q; rows that no entry owns are
- * not written, rows of a skipped entry are zero.  Entries may list the same
- * sequence and must not own the same row.
+ * not written, rows of a skipped entry are zero (of an entry whose row range or row_count is
+ * refused: not written).  Entries may list the same sequence and must not own the same row.
+ * max_rows or total_rows 0: a no-op, whatever row_count holds (here and in
+ * dflash_pages_write).
  * Cached rows past the last position, and rows that no query row of the call sees,
  * may hold anything, NaN included; a V row that one query row of an entry sees and
- * another does not must be finite.
+ * another does not must be finite.  bf16 pools want |t_k| below 2^31: beyond, one
+ * rounding of t_k in fp32 is a factor of 2^128, and rows may come out as NaN.
  * Device errors: INVALID_ARG (row ranges, row_count > max_rows or negative),
  * CAPACITY (positions without a page), UNSUPPORTED (bf16: 2^31 or more tiles of 64
- * keys over all rows and heads of the call; nothing is written). */
+ * keys over all rows and heads of the call; no result is written). */
 int dflash_paged_attention(dflash_pool* p, const int32_t* seqs, int n, int layer, const void* q, int64_t q_stride,
                            const int32_t* row_start, const int32_t* row_count, int total_rows, int max_rows,
                            int causal, int window, int sinks, void* out, dflash_stream stream);
